@@ -414,6 +414,102 @@ int bitdelta_monosoup_merge(const uint16_t* const* w_ft, int32_t k, const uint16
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Decoder-layer operators beside the linears: the norm of the residual
+ * stream, the paged key/value cache that the fused QKV rows go to, and
+ * attention over it.  bf16 tensors here need the alignment of their elements
+ * only (2 bytes); caches, 8-bit outputs and the workspace 16 bytes.  A call
+ * of no rows or tokens returns BITDELTA_OK and enqueues nothing.
+ *
+ * Groups in 8 bits: e4m3 values (OCP, no infinities) with one power-of-two
+ * scale in e8m0 (a byte e + 127).  The scale is the smallest 2^e with
+ * max|x| <= 448 * 2^e, e kept within -120..120 (-120 for a group of zeros);
+ * magnitudes above 240 * 2^120 (infinities among them) are held to it, NaN
+ * becomes e4m3's NaN and has no part in the scale.
+ *
+ * bitdelta_rms_norm - h = x + residual; y = h / sqrt(mean(h^2) + eps) * w.
+ * Sums are float32, taken of the unrounded h.  Without a residual (NULL, with
+ * h_out NULL) h is x.
+ *   x, residual   device, bf16 [rows, cols], rows x_stride / r_stride
+ *                 elements apart
+ *   w             device, bf16 [cols]
+ *   h_out, y      device, bf16 [rows, cols], written
+ * rows below 2^31, cols 1..2^30, rows * cols below 2^40.
+ *
+ * bitdelta_rms_norm_mx - the same with y in 8 bits:
+ *   y             device, e4m3 [rows, cols], written; cols % 32 == 0
+ *   scale         device, e8m0 [rows, cols / 32], written
+ */
+int bitdelta_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual,
+                      int64_t r_stride, const uint16_t* w, float eps, int64_t rows, int64_t cols,
+                      uint16_t* h_out, uint16_t* y, void* stream);
+int bitdelta_rms_norm_mx(const uint16_t* x, int64_t x_stride, const uint16_t* residual,
+                         int64_t r_stride, const uint16_t* w, float eps, int64_t rows,
+                         int64_t cols, uint16_t* h_out, uint8_t* y, uint8_t* scale, void* stream);
+
+/*
+ * Paged cache: k_cache and v_cache are [pages, heads, page, dim], bf16 or
+ * e4m3; the 8-bit form has k_scale and v_scale, e8m0 [pages, heads, page], one
+ * per row (a token's dim values of one head).  The scales are NULL for bf16.
+ * Slot s is row s % page of page s / page.  dim is 64 or 128, page a multiple
+ * of 16 up to 65536, heads 1..1024, pages * page below 2^31.
+ *
+ * bitdelta_kv_write puts row t of k and v into slot slots[t]; a slot outside
+ * the cache (a negative one for padding) is passed over, and of tokens with
+ * one slot any may stay.  k, v: device, bf16 [tokens, heads, dim], tokens and
+ * heads the given strides (in elements) apart, the dims contiguous.
+ *
+ * bitdelta_kv_read writes the rows at slots[t] to k and v, bf16
+ * [tokens, heads, dim]; a slot outside the cache gives NaN.  Every e4m3 value
+ * times its scale is a bf16 number (or rounds to a subnormal one).
+ */
+int bitdelta_kv_write(const uint16_t* k, const uint16_t* v, int64_t k_token_stride,
+                      int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                      const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim,
+                      int64_t pages, int64_t page, void* k_cache, void* v_cache,
+                      uint8_t* k_scale, uint8_t* v_scale, void* stream);
+int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim,
+                     int64_t pages, int64_t page, const void* k_cache, const void* v_cache,
+                     const uint8_t* k_scale, const uint8_t* v_scale, uint16_t* k, uint16_t* v,
+                     void* stream);
+
+/*
+ * bitdelta_paged_attention - causal attention of new tokens over the cache.
+ * Sequence b has the rows cu_q[b] .. cu_q[b+1]-1 of q (n of them) and
+ * kv_len[b] cached keys, the new tokens' own among them: key j lies in row
+ * j % page of page table[b, j / page].  Row i of the sequence stands at
+ * p = kv_len[b] - n + i and sees the keys j <= p, with window > 0 only
+ * j > p - window:
+ *   out[i] = sum_j softmax_j(scale * q[i] . k[j]) v[j]
+ * Query head h reads key/value head h / (heads / kv_heads).  A row that sees
+ * no key is zero.  Scores, maxima and sums are float32; the probabilities
+ * are rounded to bf16 for the product with v.
+ *   q         device, bf16 [tokens, heads, dim], strides in elements
+ *   table     device, int32 [seqs, width]; entries of pages that no row sees
+ *             are not read.  A page outside [0, pages) that a row sees makes
+ *             that row, and others computed with it, NaN; nothing out of
+ *             bounds is read.  kv_len is held to width * page.
+ *   cu_q      device, int32 [seqs + 1], rising; held to [0, tokens].  Rows of
+ *             out that no sequence has are not written.
+ *   max_q     the largest n; rows past it may not be computed
+ *   out       device, bf16 [tokens, heads, dim], contiguous, written
+ *   workspace device, >= bitdelta_paged_attention_workspace_size(...) bytes
+ *             (0 bytes: may be NULL); contents are scratch
+ * heads is a multiple of kv_heads, at most 1024 and 64 times kv_heads; tokens
+ * times heads and width * page below 2^31, seqs at most 65535.
+ */
+size_t bitdelta_paged_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t max_q,
+                                               int64_t heads, int64_t kv_heads, int64_t dim,
+                                               int64_t width, int64_t page);
+int bitdelta_paged_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                             const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                             const uint8_t* v_scale, const int32_t* table, const int32_t* cu_q,
+                             const int32_t* kv_len, int64_t tokens, int64_t seqs, int64_t max_q,
+                             int64_t heads, int64_t kv_heads, int64_t dim, int64_t pages,
+                             int64_t page, int64_t width, float scale, int64_t window,
+                             uint16_t* out, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
  * Calibration probes - measured ceilings for the rooflines of the kernels
  * above (they compute nothing of the method).
  *

@@ -39,3 +39,11 @@ from .bitdelta import (  # noqa: F401
     status_string,
 )
 from .deltafile import delta_blob, load_delta, read_delta_header, save_delta  # noqa: F401
+from .layer import (  # noqa: F401
+    kv_read,
+    kv_write,
+    paged_attention,
+    paged_attention_workspace_size,
+    rms_norm,
+    rms_norm_mx,
+)

@@ -64,6 +64,12 @@ EXPORTS = (
     "bitdelta_router_pending",
     "bitdelta_monosoup_workspace_size",
     "bitdelta_monosoup_merge",
+    "bitdelta_rms_norm",
+    "bitdelta_rms_norm_mx",
+    "bitdelta_kv_write",
+    "bitdelta_kv_read",
+    "bitdelta_paged_attention_workspace_size",
+    "bitdelta_paged_attention",
     "bitdelta_probe_stream_read",
     "bitdelta_probe_mfma_bf16",
     "bitdelta_probe_decode_loads",
@@ -149,6 +155,20 @@ def lib() -> ctypes.CDLL:
     L.bitdelta_monosoup_merge.argtypes = [vp, ctypes.c_int32, vp, i64, i64, ctypes.c_int32,
                                           ctypes.c_int32, vp, vp, vp, vp, sz, vp]
     L.bitdelta_monosoup_merge.restype = i32
+    f32 = ctypes.c_float
+    L.bitdelta_rms_norm.argtypes = [vp, i64, vp, i64, vp, f32, i64, i64, vp, vp, vp]
+    L.bitdelta_rms_norm.restype = i32
+    L.bitdelta_rms_norm_mx.argtypes = [vp, i64, vp, i64, vp, f32, i64, i64, vp, vp, vp, vp]
+    L.bitdelta_rms_norm_mx.restype = i32
+    L.bitdelta_kv_write.argtypes = [vp, vp] + [i64] * 4 + [vp] + [i64] * 5 + [vp] * 5
+    L.bitdelta_kv_write.restype = i32
+    L.bitdelta_kv_read.argtypes = [vp] + [i64] * 5 + [vp] * 7
+    L.bitdelta_kv_read.restype = i32
+    L.bitdelta_paged_attention_workspace_size.argtypes = [i64] * 8
+    L.bitdelta_paged_attention_workspace_size.restype = sz
+    L.bitdelta_paged_attention.argtypes = ([vp, i64, i64] + [vp] * 7 + [i64] * 9 + [f32, i64] +
+                                           [vp, vp, sz, vp])
+    L.bitdelta_paged_attention.restype = i32
     L.bitdelta_probe_stream_read.argtypes = [vp, sz, ctypes.c_int32, vp, vp]
     L.bitdelta_probe_stream_read.restype = i32
     L.bitdelta_probe_mfma_bf16.argtypes = [ctypes.c_int32, ctypes.c_int32, vp, vp]

@@ -8,6 +8,7 @@
 #include "bitdelta.h"
 #include "common.h"
 #include "internal.h"
+#include "layer.h"
 #include "probe.h"
 #include "scale_round.h"
 
@@ -66,8 +67,8 @@ BD_EXPORT const char* bitdelta_status_string(int status) {
     case BITDELTA_OK: return "ok";
     case BITDELTA_ERR_NULL: return "a required pointer is NULL";
     case BITDELTA_ERR_SHAPE:
-      return "shape out of range (need M >= 1, d_out >= 1, d_in >= 64, d_in % 64 == 0, "
-             "each below 2^31, d_out*d_in below 2^40)";
+      return "shape out of range (linears: need M >= 1, d_out >= 1, d_in >= 64, d_in % 64 == 0, "
+             "each below 2^31, d_out*d_in below 2^40; other calls: the limits of their entry)";
     case BITDELTA_ERR_ALIGN: return "a buffer is not 16-byte aligned";
     case BITDELTA_ERR_MODE: return "alpha_mode must be 0 (per matrix) or 1 (per row)";
     case BITDELTA_ERR_VARIANTS: return "n_variants must be in [1, 64]";
@@ -356,6 +357,270 @@ BD_EXPORT int bitdelta_monosoup_merge(const uint16_t* const* w_ft, int32_t k,
   return status_of(bd::launch_monosoup(w_ft, k, w_base, (int)d_out, (int)d_in, rank, power_iters,
                                        omega, w_merged, tau_mean, workspace,
                                        static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ layer operators
+namespace {
+
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Bytes from the first to past the last element of a strided bf16 tensor.
+size_t span(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t inner) {
+  return (size_t)((n0 - 1) * s0 + (n1 - 1) * s1 + inner) * 2u;
+}
+
+int rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, int64_t r_stride,
+             const uint16_t* w, float eps, int64_t rows, int64_t cols, uint16_t* h_out, void* y,
+             uint8_t* scale, bool mx, void* stream) {
+  if (rows < 0 || rows > kInt32Max || cols < 1 || cols > kMaxDin || rows * cols >= kMaxElems ||
+      (mx && cols % 32 != 0))
+    return BITDELTA_ERR_SHAPE;
+  if (rows == 0) return BITDELTA_OK;
+  if (!x || !w || !y || (residual != nullptr) != (h_out != nullptr) || (mx && !scale))
+    return BITDELTA_ERR_NULL;
+  if (x_stride < 0 || (residual && r_stride < 0) || x_stride >= kMaxElems ||
+      (residual && r_stride >= kMaxElems))
+    return BITDELTA_ERR_SHAPE;
+  if (!aligned2(x) || !aligned2(w) || !aligned2(residual) || !aligned2(h_out) ||
+      (mx ? !aligned16(y) : !aligned2(y)))
+    return BITDELTA_ERR_ALIGN;
+  const size_t n = (size_t)rows * (size_t)cols;
+  const void* outs[3] = {y, h_out, scale};
+  const size_t outn[3] = {mx ? n : 2 * n, 2 * n, n / 32};
+  const void* ins[3] = {x, residual, w};
+  const size_t inn[3] = {span(rows, x_stride, 1, 0, cols), span(rows, r_stride, 1, 0, cols),
+                         (size_t)cols * 2u};
+  for (int i = 0; i < 3; ++i) {
+    if (!outs[i]) continue;
+    for (int j = 0; j < 3; ++j)
+      if (ins[j] && overlap(outs[i], outn[i], ins[j], inn[j])) return BITDELTA_ERR_OVERLAP;
+    for (int j = i + 1; j < 3; ++j)
+      if (outs[j] && overlap(outs[i], outn[i], outs[j], outn[j])) return BITDELTA_ERR_OVERLAP;
+  }
+  const int dev = check_device();
+  if (dev != BITDELTA_OK) return dev;
+  bd::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.w = w;
+  a.h = h_out;
+  a.y = y;
+  a.scale = scale;
+  a.x_stride = x_stride;
+  a.r_stride = r_stride;
+  a.rows = rows;
+  a.cols = (int)cols;
+  a.eps = eps;
+  return status_of(bd::launch_rms_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+bool cache_shape_ok(int64_t heads, int64_t dim, int64_t pages, int64_t page) {
+  return heads >= 1 && heads <= 1024 && (dim == 64 || dim == 128) && page >= 16 &&
+         page % 16 == 0 && page <= 65536 && pages >= 1 && pages <= kInt32Max / page;
+}
+
+}  // namespace
+
+BD_EXPORT int bitdelta_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual,
+                                int64_t r_stride, const uint16_t* w, float eps, int64_t rows,
+                                int64_t cols, uint16_t* h_out, uint16_t* y, void* stream) {
+  return rms_norm(x, x_stride, residual, r_stride, w, eps, rows, cols, h_out, y, nullptr, false,
+                  stream);
+}
+
+BD_EXPORT int bitdelta_rms_norm_mx(const uint16_t* x, int64_t x_stride, const uint16_t* residual,
+                                   int64_t r_stride, const uint16_t* w, float eps, int64_t rows,
+                                   int64_t cols, uint16_t* h_out, uint8_t* y, uint8_t* scale,
+                                   void* stream) {
+  return rms_norm(x, x_stride, residual, r_stride, w, eps, rows, cols, h_out, y, scale, true,
+                  stream);
+}
+
+BD_EXPORT int bitdelta_kv_write(const uint16_t* k, const uint16_t* v, int64_t k_token_stride,
+                                int64_t k_head_stride, int64_t v_token_stride,
+                                int64_t v_head_stride, const int32_t* slots, int64_t tokens,
+                                int64_t heads, int64_t dim, int64_t pages, int64_t page,
+                                void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                                void* stream) {
+  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  if (!cache_shape_ok(heads, dim, pages, page) || tokens < 0 || tokens > kInt32Max ||
+      tokens * heads * dim >= kMaxElems)
+    return BITDELTA_ERR_SHAPE;
+  for (int64_t s : strides)
+    if (s < 0 || s >= kMaxElems) return BITDELTA_ERR_SHAPE;
+  if (tokens == 0) return BITDELTA_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache || (k_scale != nullptr) != (v_scale != nullptr))
+    return BITDELTA_ERR_NULL;
+  if (!aligned2(k) || !aligned2(v) || !aligned4(slots) || !aligned16(k_cache) ||
+      !aligned16(v_cache))
+    return BITDELTA_ERR_ALIGN;
+  const size_t rows = (size_t)pages * (size_t)page * (size_t)heads;
+  const size_t cbytes = rows * (size_t)dim * (k_scale ? 1u : 2u);
+  const void* outs[4] = {k_cache, v_cache, k_scale, v_scale};
+  const size_t outn[4] = {cbytes, cbytes, rows, rows};
+  const void* ins[3] = {k, v, slots};
+  const size_t inn[3] = {span(tokens, k_token_stride, heads, k_head_stride, dim),
+                         span(tokens, v_token_stride, heads, v_head_stride, dim),
+                         (size_t)tokens * 4u};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i]) continue;
+    for (int j = 0; j < 3; ++j)
+      if (overlap(outs[i], outn[i], ins[j], inn[j])) return BITDELTA_ERR_OVERLAP;
+    for (int j = i + 1; j < 4; ++j)
+      if (outs[j] && overlap(outs[i], outn[i], outs[j], outn[j])) return BITDELTA_ERR_OVERLAP;
+  }
+  const int dev = check_device();
+  if (dev != BITDELTA_OK) return dev;
+  bd::KvArgs a{};
+  a.src[0] = k;
+  a.src[1] = v;
+  a.cache[0] = k_cache;
+  a.cache[1] = v_cache;
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.slots = slots;
+  a.token_stride[0] = k_token_stride;
+  a.token_stride[1] = v_token_stride;
+  a.head_stride[0] = k_head_stride;
+  a.head_stride[1] = v_head_stride;
+  a.tokens = tokens;
+  a.n_slots = pages * page;
+  a.heads = (int)heads;
+  a.dim = (int)dim;
+  a.page = (int)page;
+  return status_of(bd::launch_kv_write(a, static_cast<hipStream_t>(stream)));
+}
+
+BD_EXPORT int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim,
+                               int64_t pages, int64_t page, const void* k_cache,
+                               const void* v_cache, const uint8_t* k_scale,
+                               const uint8_t* v_scale, uint16_t* k, uint16_t* v, void* stream) {
+  if (!cache_shape_ok(heads, dim, pages, page) || tokens < 0 || tokens > kInt32Max ||
+      tokens * heads * dim >= kMaxElems)
+    return BITDELTA_ERR_SHAPE;
+  if (tokens == 0) return BITDELTA_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache || (k_scale != nullptr) != (v_scale != nullptr))
+    return BITDELTA_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(slots) || !aligned16(k_cache) ||
+      !aligned16(v_cache))
+    return BITDELTA_ERR_ALIGN;
+  const size_t rows = (size_t)pages * (size_t)page * (size_t)heads;
+  const size_t cbytes = rows * (size_t)dim * (k_scale ? 1u : 2u);
+  const size_t obytes = (size_t)(tokens * heads * dim) * 2u;
+  const void* ins[5] = {k_cache, v_cache, k_scale, v_scale, slots};
+  const size_t inn[5] = {cbytes, cbytes, rows, rows, (size_t)tokens * 4u};
+  for (int j = 0; j < 5; ++j)
+    if (ins[j] && (overlap(k, obytes, ins[j], inn[j]) || overlap(v, obytes, ins[j], inn[j])))
+      return BITDELTA_ERR_OVERLAP;
+  if (overlap(k, obytes, v, obytes)) return BITDELTA_ERR_OVERLAP;
+  const int dev = check_device();
+  if (dev != BITDELTA_OK) return dev;
+  bd::KvArgs a{};
+  a.dst[0] = k;
+  a.dst[1] = v;
+  a.cache[0] = const_cast<void*>(k_cache);
+  a.cache[1] = const_cast<void*>(v_cache);
+  a.scale[0] = const_cast<uint8_t*>(k_scale);
+  a.scale[1] = const_cast<uint8_t*>(v_scale);
+  a.slots = slots;
+  a.tokens = tokens;
+  a.n_slots = pages * page;
+  a.heads = (int)heads;
+  a.dim = (int)dim;
+  a.page = (int)page;
+  return status_of(bd::launch_kv_read(a, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+bool attention_shape_ok(int64_t tokens, int64_t seqs, int64_t max_q, int64_t heads,
+                        int64_t kv_heads, int64_t dim, int64_t width, int64_t page) {
+  return cache_shape_ok(kv_heads, dim, 1, page) && heads >= kv_heads && heads <= 1024 &&
+         heads % kv_heads == 0 && heads / kv_heads <= 64 && tokens >= 0 &&
+         tokens <= kInt32Max / heads && seqs >= 0 && seqs <= 65535 && max_q >= 0 &&
+         max_q <= kInt32Max / heads && width >= 0 && width <= kInt32Max / page;
+}
+
+bd::AttnArgs attention_sizes(int64_t tokens, int64_t seqs, int64_t max_q, int64_t heads,
+                             int64_t kv_heads, int64_t dim, int64_t width, int64_t page) {
+  bd::AttnArgs a{};
+  a.tokens = (int)tokens;
+  a.seqs = (int)seqs;
+  a.max_q = (int)(max_q < tokens ? max_q : tokens);
+  a.heads = (int)heads;
+  a.kv_heads = (int)kv_heads;
+  a.group = (int)(heads / kv_heads);
+  a.dim = (int)dim;
+  a.width = (int)width;
+  a.page = (int)page;
+  return a;
+}
+
+}  // namespace
+
+BD_EXPORT size_t bitdelta_paged_attention_workspace_size(int64_t tokens, int64_t seqs,
+                                                         int64_t max_q, int64_t heads,
+                                                         int64_t kv_heads, int64_t dim,
+                                                         int64_t width, int64_t page) {
+  if (!attention_shape_ok(tokens, seqs, max_q, heads, kv_heads, dim, width, page)) return 0;
+  return bd::paged_attention_workspace(
+      attention_sizes(tokens, seqs, max_q, heads, kv_heads, dim, width, page));
+}
+
+BD_EXPORT int bitdelta_paged_attention(
+    const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+    const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* table,
+    const int32_t* cu_q, const int32_t* kv_len, int64_t tokens, int64_t seqs, int64_t max_q,
+    int64_t heads, int64_t kv_heads, int64_t dim, int64_t pages, int64_t page, int64_t width,
+    float scale, int64_t window, uint16_t* out, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  if (!attention_shape_ok(tokens, seqs, max_q, heads, kv_heads, dim, width, page) ||
+      !cache_shape_ok(kv_heads, dim, pages, page) || window < 0 || q_token_stride < 0 ||
+      q_head_stride < 0 || q_token_stride >= kMaxElems || q_head_stride >= kMaxElems)
+    return BITDELTA_ERR_SHAPE;
+  if (tokens == 0 || seqs == 0 || max_q == 0) return BITDELTA_OK;
+  if (!q || !k_cache || !v_cache || (!table && width > 0) || !cu_q || !kv_len || !out ||
+      (k_scale != nullptr) != (v_scale != nullptr))
+    return BITDELTA_ERR_NULL;
+  if (!aligned2(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) ||
+      !aligned16(v_scale) || !aligned4(table) || !aligned4(cu_q) || !aligned4(kv_len) ||
+      !aligned16(out) || !aligned16(workspace))
+    return BITDELTA_ERR_ALIGN;
+  bd::AttnArgs a = attention_sizes(tokens, seqs, max_q, heads, kv_heads, dim, width, page);
+  const size_t need = bd::paged_attention_workspace(a);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return BITDELTA_ERR_WORKSPACE;
+  const size_t rows = (size_t)pages * (size_t)page * (size_t)kv_heads;
+  const size_t cbytes = rows * (size_t)dim * (k_scale ? 1u : 2u);
+  const void* outs[2] = {out, need ? workspace : nullptr};
+  const size_t outn[2] = {(size_t)(tokens * heads * dim) * 2u, need};
+  const void* ins[8] = {q, k_cache, v_cache, k_scale, v_scale, table, cu_q, kv_len};
+  const size_t inn[8] = {span(tokens, q_token_stride, heads, q_head_stride, dim), cbytes, cbytes,
+                         rows, rows, (size_t)(seqs * width) * 4u, (size_t)(seqs + 1) * 4u,
+                         (size_t)seqs * 4u};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 8; ++j)
+      if (outs[i] && ins[j] && overlap(outs[i], outn[i], ins[j], inn[j]))
+        return BITDELTA_ERR_OVERLAP;
+  if (outs[1] && overlap(outs[0], outn[0], outs[1], outn[1])) return BITDELTA_ERR_OVERLAP;
+  const int dev = check_device();
+  if (dev != BITDELTA_OK) return dev;
+  a.q = q;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.cache[0] = static_cast<const uint8_t*>(k_cache);
+  a.cache[1] = static_cast<const uint8_t*>(v_cache);
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.table = table;
+  a.cu_q = cu_q;
+  a.kv_len = kv_len;
+  a.pages = pages;
+  a.window = (int)(window < kInt32Max ? window : kInt32Max);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = out;
+  a.partial = static_cast<float*>(workspace);
+  return status_of(bd::launch_paged_attention(a, static_cast<hipStream_t>(stream)));
 }
 
 BD_EXPORT int bitdelta_probe_stream_read(const void* src, size_t bytes, int32_t workgroups,

@@ -1,0 +1,59 @@
+// Launchers of the decoder-layer operators beside the linears: the norm of
+// the residual stream, the paged key/value cache and attention over it.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace bd {
+
+// y = h / sqrt(mean(h^2) + eps) * w of each row, h = x + residual.  scale !=
+// nullptr: y is e4m3 with one e8m0 scale per 32 values.
+struct NormArgs {
+  const uint16_t* x;         // [rows, cols], rows x_stride apart
+  const uint16_t* residual;  // the same, r_stride apart, or nullptr
+  const uint16_t* w;         // [cols]
+  uint16_t* h;               // [rows, cols] or nullptr (no residual)
+  void* y;                   // [rows, cols] bf16 or e4m3
+  uint8_t* scale;            // [rows, cols / 32] or nullptr
+  int64_t x_stride, r_stride;
+  int64_t rows;
+  int cols;
+  float eps;
+};
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream);
+
+// Rows of the cache at `slots`.  Caches are [pages, heads, page, dim]; slot s
+// is row s % page of page s / page.
+struct KvArgs {
+  const uint16_t* src[2];    // write: k, v [tokens, heads, dim] with strides
+  uint16_t* dst[2];          // read: k, v [tokens, heads, dim]
+  void* cache[2];
+  uint8_t* scale[2];         // e8m0 [pages, heads, page], nullptr for bf16
+  const int32_t* slots;      // [tokens]
+  int64_t token_stride[2], head_stride[2];
+  int64_t tokens, n_slots;
+  int heads, dim, page;
+};
+hipError_t launch_kv_write(const KvArgs& a, hipStream_t stream);
+hipError_t launch_kv_read(const KvArgs& a, hipStream_t stream);
+
+struct AttnArgs {
+  const uint16_t* q;         // [tokens, heads, dim] with strides
+  const uint8_t* cache[2];   // k, v: [pages, kv_heads, page, dim]
+  const uint8_t* scale[2];   // e8m0 [pages, kv_heads, page], nullptr for bf16
+  const int32_t* table;      // [seqs, width] page ids
+  const int32_t* cu_q;       // [seqs + 1]
+  const int32_t* kv_len;     // [seqs]
+  uint16_t* out;             // [tokens, heads, dim]
+  float* partial;            // workspace
+  int64_t q_token_stride, q_head_stride;
+  int64_t pages;
+  int tokens, seqs, max_q, heads, kv_heads, group, dim, page, width;
+  int window;                // 0: none
+  float scale_log2;          // softmax scale * log2(e)
+};
+size_t paged_attention_workspace(const AttnArgs& a);
+hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream);
+
+}  // namespace bd

@@ -1,0 +1,210 @@
+// Root-mean-square norm of the residual stream.
+//
+//   h = x + residual          (float32; written back rounded to bf16)
+//   y = h / sqrt(mean(h^2) + eps) * w
+//
+// y is bf16, or e4m3 with one power-of-two scale per 32 values.  The norm is
+// taken of the unrounded float32 sum, so the only roundings are those of the
+// outputs.  Bound by HBM: 2 bytes in per value and input, 2 (or 1 + 1/32) out;
+// a row stays in registers between its sum of squares and its output, so each
+// value is read once.
+#include "common.h"
+#include "e4m3.h"
+#include "layer.h"
+
+namespace bd {
+namespace {
+
+// 16 bytes at an address aligned to its 2-byte elements only (rows of an odd
+// length, strided rows): one load or store of the full width all the same.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+__device__ __forceinline__ u32x4 ld8(const uint16_t* p) {
+  return *reinterpret_cast<const u32x4_any*>(p);
+}
+__device__ __forceinline__ void st8(uint16_t* p, u32x4 v) {
+  *reinterpret_cast<u32x4_any*>(p) = v;
+}
+
+__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// Up to eight elements from p, zeros past n.
+__device__ __forceinline__ u32x4 ld_some(const uint16_t* p, int n) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) v[e >> 1] |= (uint32_t)p[e] << ((e & 1) << 4);
+  return v;
+}
+__device__ __forceinline__ void st_some(uint16_t* p, u32x4 v, int n) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) p[e] = (uint16_t)(v[e >> 1] >> ((e & 1) << 4));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Sum over the T threads of a row (T = 64, or the whole workgroup).
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum(v);
+  if (T == kWave) return v;
+  if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < T / kWave; ++i) s += red[i];
+  return s;
+}
+
+// Eight values of one row: load x (+ residual), write h, keep float32.
+template <bool RES>
+__device__ __forceinline__ void load_sum(const uint16_t* x, const uint16_t* r, uint16_t* h,
+                                         int n, float (&f)[8]) {
+  const bool all = n >= 8;
+  const u32x4 a = all ? ld8(x) : ld_some(x, n);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    f[2 * d] = lo16(a[d]);
+    f[2 * d + 1] = hi16(a[d]);
+  }
+  if (RES) {
+    const u32x4 b = all ? ld8(r) : ld_some(r, n);
+    u32x4 o;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      f[2 * d] += lo16(b[d]);
+      f[2 * d + 1] += hi16(b[d]);
+      o[d] = cvt_pk_bf16(f[2 * d], f[2 * d + 1]);
+    }
+    if (all) st8(h, o);
+    else st_some(h, o, n);
+  }
+}
+
+// Eight normalised values out.  In 8 bits four neighbouring lanes hold a
+// group of 32 and share its largest magnitude.
+template <bool MX>
+__device__ __forceinline__ void put(const NormArgs& a, int64_t row, int col, int n,
+                                    const float (&f)[8], float inv) {
+  const u32x4 w = n >= 8 ? ld8(a.w + col) : ld_some(a.w + col, n);
+  float y[8];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    y[2 * d] = f[2 * d] * inv * lo16(w[d]);
+    y[2 * d + 1] = f[2 * d + 1] * inv * hi16(w[d]);
+  }
+  if (!MX) {
+    u32x4 o;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] = cvt_pk_bf16(y[2 * d], y[2 * d + 1]);
+    uint16_t* p = static_cast<uint16_t*>(a.y) + row * a.cols + col;
+    if (n >= 8) st8(p, o);
+    else st_some(p, o, n);
+    return;
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y[e] = hold_e4m3(y[e]);
+    m = fmaxf(m, fabsf(y[e]));
+  }
+  m = fmaxf(m, __shfl_xor(m, 1));
+  m = fmaxf(m, __shfl_xor(m, 2));
+  const uint32_t sb = scale_byte(m);
+  const float is = inv_scale(sb);
+  typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
+  const u32x2 o = {pack_e4m3(y[0] * is, y[1] * is, y[2] * is, y[3] * is),
+                   pack_e4m3(y[4] * is, y[5] * is, y[6] * is, y[7] * is)};
+  *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.y) + row * a.cols + col) = o;
+  if ((threadIdx.x & 3) == 0) a.scale[row * (a.cols >> 5) + (col >> 5)] = (uint8_t)sb;
+}
+
+// T threads a row, CH groups of eight values a thread.
+template <int T, int CH, bool RES, bool MX>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(const NormArgs a) {
+  __shared__ float red[T / kWave];
+  const int t = T < 256 ? threadIdx.x & (T - 1) : threadIdx.x;
+  const int64_t row = T < 256 ? (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T : blockIdx.x;
+  if (T < 256 && row >= a.rows) return;  // whole waves
+  const uint16_t* x = a.x + row * a.x_stride;
+  const uint16_t* r = RES ? a.residual + row * a.r_stride : nullptr;
+  uint16_t* h = RES ? a.h + row * a.cols : nullptr;
+  float f[CH][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = (c * T + t) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[c][e] = 0.f;
+    if (col < a.cols) load_sum<RES>(x + col, r + col, h + col, a.cols - col, f[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(f[c][e], f[c][e], ss);
+  const float inv = rsqrtf(row_sum<T>(ss, red) / (float)a.cols + a.eps);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = (c * T + t) * 8;
+    if (col < a.cols) put<MX>(a, row, col, a.cols - col, f[c], inv);
+  }
+}
+
+// Rows too long for the registers of one workgroup: the sum is formed twice.
+template <bool RES, bool MX>
+__global__ __launch_bounds__(1024) void rms_norm_long_kernel(const NormArgs a) {
+  __shared__ float red[16];
+  const int64_t row = blockIdx.x;
+  const uint16_t* x = a.x + row * a.x_stride;
+  const uint16_t* r = RES ? a.residual + row * a.r_stride : nullptr;
+  uint16_t* h = RES ? a.h + row * a.cols : nullptr;
+  float ss = 0.f;
+  float f[8];
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 8192) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    load_sum<RES>(x + col, r + col, h + col, (int)(a.cols - col), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+  }
+  const float inv = rsqrtf(row_sum<1024>(ss, red) / (float)a.cols + a.eps);
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 8192) {
+    load_sum<RES>(x + col, r + col, h + col, (int)(a.cols - col), f);
+    put<MX>(a, row, (int)col, (int)(a.cols - col), f, inv);
+  }
+}
+
+template <bool RES, bool MX>
+hipError_t pick(const NormArgs& a, hipStream_t s) {
+  const unsigned rows = (unsigned)a.rows;
+  if (a.cols <= 512)
+    rms_norm_kernel<64, 1, RES, MX><<<(rows + 3) / 4, 256, 0, s>>>(a);
+  else if (a.cols <= 1024)
+    rms_norm_kernel<64, 2, RES, MX><<<(rows + 3) / 4, 256, 0, s>>>(a);
+  else if (a.cols <= 2048)
+    rms_norm_kernel<256, 1, RES, MX><<<rows, 256, 0, s>>>(a);
+  else if (a.cols <= 4096)
+    rms_norm_kernel<256, 2, RES, MX><<<rows, 256, 0, s>>>(a);
+  else if (a.cols <= 8192)
+    rms_norm_kernel<1024, 1, RES, MX><<<rows, 1024, 0, s>>>(a);
+  else if (a.cols <= 16384)
+    rms_norm_kernel<1024, 2, RES, MX><<<rows, 1024, 0, s>>>(a);
+  else
+    rms_norm_long_kernel<RES, MX><<<rows, 1024, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+  if (a.scale) return a.residual ? pick<true, true>(a, s) : pick<false, true>(a, s);
+  return a.residual ? pick<true, false>(a, s) : pick<false, false>(a, s);
+}
+
+}  // namespace bd
