@@ -451,7 +451,8 @@ int bitdelta_rms_norm_mx(const uint16_t* x, int64_t x_stride, const uint16_t* re
  * e4m3; the 8-bit form has k_scale and v_scale, e8m0 [pages, heads, page], one
  * per row (a token's dim values of one head).  The scales are NULL for bf16.
  * Slot s is row s % page of page s / page.  dim is 64 or 128, page a multiple
- * of 16 up to 65536, heads 1..1024, pages * page below 2^31.
+ * of 16 up to 65536, heads 1..1024, pages * page below 2^31
+ * and, times heads, at most 2^35.
  *
  * bitdelta_kv_write puts row t of k and v into slot slots[t]; a slot outside
  * the cache (a negative one for padding) is passed over, and of tokens with
@@ -495,7 +496,7 @@ int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_
  *   workspace device, >= bitdelta_paged_attention_workspace_size(...) bytes
  *             (0 bytes: may be NULL); contents are scratch
  * heads is a multiple of kv_heads, at most 1024 and 64 times kv_heads; tokens
- * times heads and width * page below 2^31, seqs at most 65535.
+ * times heads below 2^30, width * page and max_q below 2^31, seqs at most 65535.
  */
 size_t bitdelta_paged_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t max_q,
                                                int64_t heads, int64_t kv_heads, int64_t dim,

@@ -417,7 +417,8 @@ int rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, int6
 
 bool cache_shape_ok(int64_t heads, int64_t dim, int64_t pages, int64_t page) {
   return heads >= 1 && heads <= 1024 && (dim == 64 || dim == 128) && page >= 16 &&
-         page % 16 == 0 && page <= 65536 && pages >= 1 && pages <= kInt32Max / page;
+         page % 16 == 0 && page <= 65536 && pages >= 1 && pages <= kInt32Max / page &&
+         pages * page <= (int64_t(1) << 35) / heads;  // groups of 16 rows count in an int
 }
 
 }  // namespace
@@ -538,8 +539,8 @@ bool attention_shape_ok(int64_t tokens, int64_t seqs, int64_t max_q, int64_t hea
                         int64_t kv_heads, int64_t dim, int64_t width, int64_t page) {
   return cache_shape_ok(kv_heads, dim, 1, page) && heads >= kv_heads && heads <= 1024 &&
          heads % kv_heads == 0 && heads / kv_heads <= 64 && tokens >= 0 &&
-         tokens <= kInt32Max / heads && seqs >= 0 && seqs <= 65535 && max_q >= 0 &&
-         max_q <= kInt32Max / heads && width >= 0 && width <= kInt32Max / page;
+         tokens <= (kInt32Max >> 1) / heads && seqs >= 0 && seqs <= 65535 && max_q >= 0 &&
+         max_q <= kInt32Max && width >= 0 && width <= kInt32Max / page;
 }
 
 bd::AttnArgs attention_sizes(int64_t tokens, int64_t seqs, int64_t max_q, int64_t heads,

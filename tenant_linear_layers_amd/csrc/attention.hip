@@ -37,10 +37,11 @@ typedef int i32x2 __attribute__((__vector_size__(8)));
 
 // A tile of up to R rows of one sequence and the keys it can see.
 struct Tile {
-  int first_q, n_q;   // the sequence's rows of q / out and their number
+  int first_q;        // the sequence's first row of q / out
   int row0, rows;     // rows (query * group + head) of the tile
   int pos0;           // position of query 0 of the sequence
   int lo, hi;         // keys that some row of the tile sees
+  int all_lo, all_hi; // keys that every row of the tile sees
 };
 
 __device__ __forceinline__ void seq_range(const AttnArgs& a, int b, int& q0, int& n, int& len) {
@@ -52,13 +53,14 @@ __device__ __forceinline__ void seq_range(const AttnArgs& a, int b, int& q0, int
 __device__ __forceinline__ Tile tile_of(const AttnArgs& a, int q0, int n, int len, int t, int R) {
   Tile x;
   x.first_q = q0;
-  x.n_q = n;
   x.row0 = t * R;
   x.rows = min(R, n * a.group - x.row0);
   x.pos0 = len - n;
   const int i0 = x.row0 / a.group, i1 = (x.row0 + x.rows - 1) / a.group;
   x.hi = max(min(len, x.pos0 + i1 + 1), 0);
   x.lo = a.window ? max(x.pos0 + i0 - a.window + 1, 0) : 0;
+  x.all_hi = x.pos0 + i0 + 1;
+  x.all_lo = a.window ? x.pos0 + i1 - a.window + 1 : 0;
   if (x.lo >= x.hi) x.lo = x.hi = 0;
   return x;
 }
@@ -75,170 +77,458 @@ __device__ __forceinline__ float scale_of(uint32_t dword, int r) {
   return __uint_as_float(((dword >> (8 * r)) & 0xFFu) << 23);
 }
 
+// ------------------------------------------------------------------ plan
+// The lengths lie on the device, so every workgroup finds its own work: item
+// index -> (sequence b, tile, piece of the tile's keys, key/value head), heads
+// fastest, pieces next.  A sequence whose widest tile has `blocks` blocks of
+// 32 keys is cut into ceil(blocks / C) pieces a tile, with C such that all
+// items together are about `target`; each piece takes an equal share of its
+// own tile's blocks.  Then items <= target + tiles * kv_heads, which bounds
+// the grid and the workspace on the host.  Every wave computes the same plan
+// (lane by sequence, 64 at a time), and the joining kernel again.
+struct Cut {
+  int R, target, min_blocks;   // rows a tile, items aimed at, blocks a piece at least
+};
+
+struct Item {
+  int b, tile, piece, pieces, head;
+  int q0, n, len;
+  int first;                   // index of the tile's first piece, by head
+};
+
+__device__ __forceinline__ int blocks_of(const AttnArgs& a, const Cut& c, int n, int len) {
+  const int qs = min(n, c.R / a.group + 2);                 // queries that a tile can hold rows of
+  const int64_t keys = a.window ? min((int64_t)len, (int64_t)a.window + qs) : len;
+  return (int)((keys + 31) >> 5) + (a.window ? 1 : 0);
+}
+
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, const Cut& c, int n) {
+  return (n * a.group + c.R - 1) / c.R;
+}
+
+// Item idx (JOIN: tile idx, its first piece); false past the last one.
+template <bool JOIN>
+__device__ bool find_item(const AttnArgs& a, const Cut& c, int idx, Item& it) {
+  const int lane = threadIdx.x & 63;
+  it.head = idx % a.kv_heads;
+  const int want = idx / a.kv_heads;
+  float load = 0.f;
+  int q0 = 0, n = 0, len = 0, tiles = 0, blocks = 0;
+  for (int b0 = 0; b0 < a.seqs; b0 += 64) {
+    float mine = 0.f;
+    if (b0 + lane < a.seqs) {
+      seq_range(a, b0 + lane, q0, n, len);
+      tiles = tiles_of(a, c, n);
+      blocks = blocks_of(a, c, n, len);
+      mine = (float)tiles * (float)blocks;
+    }
+    if (a.seqs == 1) {
+      load = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(mine)));
+    } else {
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(mine, o);
+      load += mine;
+    }
+  }
+  const int C = max((int)fminf(load * (float)a.kv_heads / (float)c.target, 1e9f) + 1, c.min_blocks);
+  int before = 0, first = 0;   // tiles (JOIN) or items before this chunk; items before it
+  for (int b0 = 0; b0 < a.seqs; b0 += 64) {
+    int pieces = 1, items = 0, at = 0, tl = 0;
+    if (b0 + lane < a.seqs) {
+      if (a.seqs > 64) {
+        seq_range(a, b0 + lane, q0, n, len);
+        tiles = tiles_of(a, c, n);
+        blocks = blocks_of(a, c, n, len);
+      }
+      pieces = max((blocks + C - 1) / C, 1);
+      items = tiles * pieces;
+      tl = tiles;
+    }
+    int sum = JOIN ? tl : items, isum = items;
+    if (a.seqs > 1) {
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(sum, o), iup = JOIN ? __shfl_up(isum, o) : 0;
+        if (lane >= o) {
+          sum += up;
+          isum += iup;
+        }
+      }
+    }
+    if (!JOIN) isum = sum;
+    const int width = JOIN ? tl : items;
+    at = before + sum - width;
+    const uint64_t hit = __ballot(want >= at && want < at + width);
+    if (hit) {
+      const int src = __builtin_ctzll(hit);
+      it.b = b0 + src;
+      it.head = __builtin_amdgcn_readfirstlane(it.head);
+      it.pieces = __builtin_amdgcn_readlane(pieces, src);
+      it.q0 = __builtin_amdgcn_readlane(q0, src);
+      it.n = __builtin_amdgcn_readlane(n, src);
+      it.len = __builtin_amdgcn_readlane(len, src);
+      const int local = want - __builtin_amdgcn_readlane(at, src);
+      it.tile = JOIN ? local : local / it.pieces;
+      it.piece = JOIN ? 0 : local - it.tile * it.pieces;
+      it.first = first + __builtin_amdgcn_readlane(isum - items, src) + it.tile * it.pieces;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+    first += __builtin_amdgcn_readlane(isum, 63);
+  }
+  return false;
+}
+
+// Keys [lo, hi) of a piece: its share of the tile's blocks of 32.
+__device__ __forceinline__ void piece_range(const Tile& t, int piece, int pieces, int& lo,
+                                            int& hi) {
+  const int b0 = t.lo >> 5, nb = t.hi > t.lo ? ((t.hi + 31) >> 5) - b0 : 0;
+  lo = max((b0 + (int)((int64_t)nb * piece / pieces)) << 5, t.lo);
+  hi = min((b0 + (int)((int64_t)nb * (piece + 1) / pieces)) << 5, t.hi);
+  if (nb == 0) lo = hi = 0;
+}
+
+// Sums of the pieces: [item][R][D] floats, then [item][R] (m, l).
+__device__ __forceinline__ float* sums_at(const AttnArgs& a, const Cut& c, int D, int item) {
+  return a.partial + (size_t)item * c.R * D;
+}
+__device__ __forceinline__ float* ml_at(const AttnArgs& a, const Cut& c, int D, int item) {
+  return a.partial + (size_t)a.items * c.R * D + (size_t)item * c.R * 2;
+}
+
+// One wave a row: the row's pieces added up, in the order of their keys.
+template <int D>
+__global__ __launch_bounds__(256) void join_pieces_kernel(const AttnArgs a, const Cut c) {
+  const int per = (c.R + 3) / 4;
+  Item it;
+  if (!find_item<true>(a, c, blockIdx.x / per, it) || it.pieces == 1) return;
+  // cu_q that does not rise could ask for more items than there are
+  if ((it.first + it.pieces) * a.kv_heads > a.items) return;
+  const int lane = threadIdx.x & 63;
+  const int row = (blockIdx.x % per) * 4 + (threadIdx.x >> 6);
+  const int r = it.tile * c.R + row;
+  if (row >= c.R || r >= it.n * a.group) return;
+  const int item0 = it.first * a.kv_heads + it.head;
+  float top = -INFINITY;
+  for (int p = lane; p < it.pieces; p += 64)
+    top = fmaxf(top, ml_at(a, c, D, item0 + p * a.kv_heads)[row * 2]);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  const float ref = top == -INFINITY ? 0.f : top;
+  constexpr int N = D / 64;
+  float tot = 0.f, v[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < it.pieces; ++p) {
+    const int item = item0 + p * a.kv_heads;
+    const float* ml = ml_at(a, c, D, item) + row * 2;
+    const float f = __builtin_amdgcn_exp2f(ml[0] - ref);
+    tot = fmaf(f, ml[1], tot);
+    const float* s = sums_at(a, c, D, item) + (size_t)row * D + lane * N;
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = fmaf(f, s[e], v[e]);
+  }
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
+  const int i = r / a.group;
+  uint16_t* o = a.out + ((int64_t)(it.q0 + i) * a.heads + it.head * a.group + r - i * a.group) * D +
+                lane * N;
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] = f32_to_bf16_bits(v[e] * inv);
+}
+
+// ------------------------------------------------------------------ reads of V
+// Transposing LDS reads: 16 lanes read 8 bytes each, together a block of four
+// rows of 16 bf16 (eight rows of 16 bytes), and lane n of them gets column n.
+// Several at once, their wait in the same statement: the builtins would also
+// wait for every load to LDS in flight, the next steps' among them.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(BD_LDS const char*)p;
+}
+
+// Blocks of four rows at four addresses and OFF bytes after each.
+template <int OFF>
+__device__ __forceinline__ void read_tr16(const uint32_t (&at)[4], u32x4 (&v)[4]) {
+  u32x2 r[8];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8\n"
+      "ds_read_b64_tr_b16 %1, %8 offset:%12\n"
+      "ds_read_b64_tr_b16 %2, %9\n"
+      "ds_read_b64_tr_b16 %3, %9 offset:%12\n"
+      "ds_read_b64_tr_b16 %4, %10\n"
+      "ds_read_b64_tr_b16 %5, %10 offset:%12\n"
+      "ds_read_b64_tr_b16 %6, %11\n"
+      "ds_read_b64_tr_b16 %7, %11 offset:%12\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]),
+        "=&v"(r[6]), "=&v"(r[7])
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = u32x4{r[2 * i][0], r[2 * i][1], r[2 * i + 1][0], r[2 * i + 1][1]};
+}
+
+__device__ __forceinline__ void read_tr8(const uint32_t (&at)[4], u32x2 (&r)[4]) {
+  asm volatile(
+      "ds_read_b64_tr_b8 %0, %4\n"
+      "ds_read_b64_tr_b8 %1, %5\n"
+      "ds_read_b64_tr_b8 %2, %6\n"
+      "ds_read_b64_tr_b8 %3, %7\n"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+      : "memory");
+}
+
 // ------------------------------------------------------------------ few rows
-// Tiles of 16 rows.  The four waves of a workgroup take 32-key steps of the
-// tile's keys in turn, each through its own part of LDS, and join at the end.
-template <int D, bool Q8>
-__global__ __launch_bounds__(256) void attend_rows16_kernel(const AttnArgs a) {
-  constexpr int R = 16, NW = 4;
+template <int N>
+__device__ __forceinline__ void wait_loads() {   // at most N vector loads in flight
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void wait_lds() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Tiles of 16 rows.  The NW waves of a workgroup take 32-key steps of the
+// piece in turn, each through its own ring of U stages in LDS: rows go there
+// straight from HBM (16 bytes a lane, whole rows in order, so a load is
+// coalesced; only the pieces of a row are permuted) and are read back as
+// matrix operands, so there is no barrier until the waves' sums are joined.
+template <int D, bool Q8, int NW, int U>
+__global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a, const Cut c) {
+  constexpr int R = 16;
   constexpr int ROWB = Q8 ? D : 2 * D;
   constexpr int P = ROWB / 16;              // 16-byte pieces of a row
   constexpr int KPI = 64 / P;               // keys per staging instruction
+  constexpr int IPH = 16 / KPI;             // staging instructions per 16 keys
+  constexpr int HALF = 2 * IPH + (Q8 ? 2 : 0);   // loads of K, and of V, per step
   constexpr int STAGE = 32 * ROWB;          // one of K, V
   constexpr int RED = NW * R * (D + 2) * 4;
-  constexpr int SMEM = NW * 2 * STAGE > RED ? NW * 2 * STAGE : RED;
+  constexpr int SMEM = NW * U * 2 * STAGE > RED ? NW * U * 2 * STAGE : RED;
   __shared__ __attribute__((aligned(16))) char smem[SMEM];
 
+  Item it;
+  if (!find_item<false>(a, c, blockIdx.x, it)) return;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g4 = lane >> 4;
-  const int head = blockIdx.x;   // key/value head
-  const int b = blockIdx.z;
-  int q0, nq, len;
-  seq_range(a, b, q0, nq, len);
-  if ((int)blockIdx.y * R >= nq * a.group) return;
-  const Tile t = tile_of(a, q0, nq, len, blockIdx.y, R);
+  const Tile t = tile_of(a, it.q0, it.n, it.len, it.tile, R);
+  int lo, hi;
+  piece_range(t, it.piece, it.pieces, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  const int kbeg = (lo & ~31) + 32 * wv;
+  const int steps = hi > kbeg ? (hi - kbeg + 32 * NW - 1) / (32 * NW) : 0;
 
   // Q^T: lane n's row, the dims that the lane's K pieces hold.
   u32x4 qf[D / 32];
   const int my = min(n, t.rows - 1);
   const int qi = (t.row0 + my) / a.group;
-  const uint16_t* qp = a.q + (int64_t)(t.first_q + qi) * a.q_token_stride +
-                       (int64_t)(head * a.group + (t.row0 + my) - qi * a.group) * a.q_head_stride;
+  const uint16_t* qp =
+      a.q + (int64_t)(t.first_q + qi) * a.q_token_stride +
+      (int64_t)(it.head * a.group + (t.row0 + my) - qi * a.group) * a.q_head_stride;
 #pragma unroll
   for (int s = 0; s < D / 32; ++s) {
     const int d0 = Q8 ? 64 * (s >> 1) + 16 * g4 + 8 * (s & 1) : 32 * s + 8 * g4;
     qf[s] = *reinterpret_cast<const u32x4_any*>(qp + d0);
   }
   const int pos = t.pos0 + qi;
-  const int vis_hi = pos + 1, vis_lo = a.window ? pos - a.window + 1 : 0;
+  const int vis_hi = min(pos + 1, hi), vis_lo = a.window ? pos - a.window + 1 : 0;
 
-  char* kst = smem + wv * 2 * STAGE;
-  char* vst = kst + STAGE;
+  char* ring = smem + wv * U * 2 * STAGE;
+  int voff[IPH];
+#pragma unroll
+  for (int j = 0; j < IPH; ++j) {
+    const int key = j * KPI + lane / P;
+    voff[j] = key * ROWB + (((lane % P) ^ swizzle<ROWB>(key)) << 4);
+  }
+  uint32_t ks[U][2], vs[U][2];
+  bool bad = false;
+  int blocks = -1;   // lane 2 i + h: rows / 16 of the cache for half h of step i (mod 32)
+
+  auto issue = [&](int i, int u, bool first) {
+    if ((i & 31) == 0) {
+      const int64_t key = (int64_t)kbeg + (int64_t)32 * NW * (i + (lane >> 1)) + 16 * (lane & 1);
+      blocks = -1;
+      if (key < hi) {
+        const int at = (int)key / a.page;
+        const int page = a.table[(int64_t)it.b * a.width + at];
+        if (page >= 0 && page < a.pages)
+          blocks = (int)((((int64_t)page * a.kv_heads + it.head) * a.page + (key - at * a.page)) >>
+                         4);
+        else  // a page that the cache lacks: the rows that see it are NaN
+          bad |= key + 16 > lo;
+      }
+    }
+    const int key0 = kbeg + 32 * NW * i;
+    char* st = ring + u * 2 * STAGE;
+    int blk[2], keys[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      blk[h] = __builtin_amdgcn_readlane(blocks, 2 * (i & 31) + h);
+      keys[h] = __builtin_amdgcn_readfirstlane(
+          blk[h] < 0 || i >= steps ? 0 : min(max(hi - key0 - 16 * h, 0), 16));
+      blk[h] = max(blk[h], 0);
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      if (Q8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          (w ? vs : ks)[u][h] =
+              bload32(a.scale[w] + (int64_t)blk[h] * 16, (keys[h] + 3) & ~3, 4 * g4, 0);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < IPH; ++j) {
+          // keys below lo read as zero (their rows may be anything), like
+          // those from hi on, which lie past the resource
+          const bool below = first && key0 + 16 * h + j * KPI + lane / P < lo;
+          lds_bload16(a.cache[w] + (int64_t)blk[h] * (16 * ROWB), keys[h] * ROWB,
+                      below ? 1 << 30 : voff[j], 0, st + w * STAGE + (h * IPH + j) * 1024);
+        }
+      }
+      // the waits below count on K's loads before V's
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
   f32x4 acc[D / 16];
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
-  bool bad = false;
 
-  for (int key0 = (t.lo & ~31) + 32 * wv; key0 < t.hi; key0 += 32 * NW) {
-    uint32_t ks[2] = {0, 0}, vs[2] = {0, 0};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k0 = key0 + 16 * h;
-      int page = 0;
-      if (k0 < t.hi) {
-        page = a.table[(int64_t)b * a.width + k0 / a.page];
-        if (page < 0 || page >= a.pages) bad = true;
-      }
-      const int keys = page < 0 || page >= a.pages ? 0 : min(max(t.hi - k0, 0), 16);
-      const int64_t row = ((int64_t)(keys ? page : 0) * a.kv_heads + head) * a.page + k0 % a.page;
-#pragma unroll
-      for (int j = 0; j < 16 / KPI; ++j) {
-        const int key = j * KPI + lane / P, piece = lane % P;
-        u32x4 kv = {0, 0, 0, 0}, vv = {0, 0, 0, 0};
-        if (key < keys && k0 + key >= t.lo) {
-          kv = ld128(a.cache[0] + (row + key) * ROWB + piece * 16);
-          vv = ld128(a.cache[1] + (row + key) * ROWB + piece * 16);
-        }
-        const int at = (16 * h + key) * ROWB + ((piece ^ swizzle<ROWB>(16 * h + key)) << 4);
-        *reinterpret_cast<u32x4*>(kst + at) = kv;
-        *reinterpret_cast<u32x4*>(vst + at) = vv;
-      }
-      if (Q8 && keys) {
-        ks[h] = ld32(a.scale[0] + row + 4 * g4);
-        vs[h] = ld32(a.scale[1] + row + 4 * g4);
-      }
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the wave's own stage is written
-    __builtin_amdgcn_sched_barrier(0);
-
+  auto step = [&](int i, int u) {
+    const int key0 = kbeg + 32 * NW * i;
+    const char* kst = ring + u * 2 * STAGE;
+    char* vst = ring + u * 2 * STAGE + STAGE;
     float s[8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       f32x4 z = {0.f, 0.f, 0.f, 0.f};
       const int key = 16 * h + n;
-      if (Q8) {
 #pragma unroll
-        for (int p = 0; p < D / 64; ++p) {
-          const u32x4 c = *reinterpret_cast<const u32x4*>(
-              kst + key * ROWB + (((4 * p + g4) ^ swizzle<ROWB>(key)) << 4));
+      for (int p = 0; p < P / 4; ++p) {
+        const u32x4 k4 = *reinterpret_cast<const u32x4*>(
+            kst + key * ROWB + (((4 * p + g4) ^ swizzle<ROWB>(key)) << 4));
+        if (Q8) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const u32x4 kf = {bf16x2_of_e4m3<false>(c[2 * e], 1.f),
-                              bf16x2_of_e4m3<true>(c[2 * e], 1.f),
-                              bf16x2_of_e4m3<false>(c[2 * e + 1], 1.f),
-                              bf16x2_of_e4m3<true>(c[2 * e + 1], 1.f)};
+            const u32x4 kf = {bf16x2_of_e4m3<false>(k4[2 * e], 1.f),
+                              bf16x2_of_e4m3<true>(k4[2 * e], 1.f),
+                              bf16x2_of_e4m3<false>(k4[2 * e + 1], 1.f),
+                              bf16x2_of_e4m3<true>(k4[2 * e + 1], 1.f)};
             z = mfma16(kf, qf[2 * p + e], z);
           }
+        } else {
+          z = mfma16(k4, qf[p], z);
         }
-      } else {
-#pragma unroll
-        for (int p = 0; p < D / 32; ++p)
-          z = mfma16(*reinterpret_cast<const u32x4*>(
-                         kst + key * ROWB + (((4 * p + g4) ^ swizzle<ROWB>(key)) << 4)),
-                     qf[p], z);
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int j = key0 + 16 * h + 4 * g4 + r;
         float v = z[r] * a.scale_log2;
-        if (Q8) v *= scale_of(ks[h], r);
-        s[4 * h + r] = j < vis_hi && j >= vis_lo && j < t.hi ? v : -INFINITY;
+        if (Q8) v *= scale_of(ks[u][h], r);
+        s[4 * h + r] = v;
+      }
+    }
+    // a mask only where some row of the tile sees part of the step
+    if (key0 + 32 > t.all_hi || key0 < t.all_lo || key0 + 32 > hi) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = key0 + 16 * (e >> 2) + 4 * g4 + (e & 3);
+        s[e] = j < vis_hi && j >= vis_lo ? s[e] : -INFINITY;
       }
     }
     float top = s[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float m1 = fmaxf(m, top);
-    const float ref = m1 == -INFINITY ? 0.f : m1;
-    const float f = __builtin_amdgcn_exp2f(m - ref);
-    m = m1;
-    l *= f;
+    // The reference moves only when a score passes it by 2^6 or more: until
+    // then the weights stay below 2^6, far from the limits of float32 and
+    // bf16, and no lane exchange or rescaling is needed.
+    if (__ballot(top > m + 6.f)) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m1 = fmaxf(m, top);
+      const float f = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m1);
+      m = m1;
+      l *= f;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) acc[i] *= f;
+      for (int d = 0; d < D / 16; ++d) acc[d] *= f;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       s[e] = __builtin_amdgcn_exp2f(s[e] - ref);
       l += s[e];
-      if (Q8) s[e] = s[e] > 0.f ? s[e] * scale_of(vs[e >> 2], e & 3) : 0.f;  // 0 past the end
+      // a weight of 0 stays 0 whatever the scale of a row that is not there
+      if (Q8) s[e] = s[e] > 0.f ? s[e] * scale_of(vs[u][e >> 2], e & 3) : 0.f;
     }
     const u32x4 pf = {cvt_pk_bf16(s[0], s[1]), cvt_pk_bf16(s[2], s[3]), cvt_pk_bf16(s[4], s[5]),
                       cvt_pk_bf16(s[6], s[7])};
+    wait_loads<HALF * 2 * (U - 1)>();
 #pragma unroll
-    for (int dt = 0; dt < D / 16; ++dt) {
-      u32x4 vf;
+    for (int d4 = 0; d4 < D / 16; d4 += 4) {   // four tiles of 16 dims
+      u32x4 vf[4];
+      uint32_t at[4];
       if (Q8) {
         // eight keys (4 g4 + 0..3 of both halves) of one dim per lane
         const int key = 16 * (n >> 3) + 4 * g4 + ((n >> 1) & 3);
-        const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (BD_LDS i32x2*)(vst + key * ROWB + ((dt ^ swizzle<ROWB>(key)) << 4) + 8 * (n & 1)));
-        vf = u32x4{bf16x2_of_e4m3<false>(c[0], 1.f), bf16x2_of_e4m3<true>(c[0], 1.f),
-                   bf16x2_of_e4m3<false>(c[1], 1.f), bf16x2_of_e4m3<true>(c[1], 1.f)};
-      } else {
-        u32x2 c[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = 16 * h + 4 * g4 + (n >> 2);
-          c[h] = __builtin_bit_cast(
-              u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((BD_LDS s16x4*)(
-                         vst + key * ROWB +
-                         (((2 * dt + ((n >> 1) & 1)) ^ swizzle<ROWB>(key)) << 4) + 8 * (n & 1))));
-        }
-        vf = u32x4{c[0][0], c[0][1], c[1][0], c[1][1]};
+        for (int e = 0; e < 4; ++e)
+          at[e] = lds_address(vst + key * ROWB + (((d4 + e) ^ swizzle<ROWB>(key)) << 4) +
+                              8 * (n & 1));
+        u32x2 v2[4];
+        read_tr8(at, v2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          vf[e] = u32x4{bf16x2_of_e4m3<false>(v2[e][0], 1.f), bf16x2_of_e4m3<true>(v2[e][0], 1.f),
+                        bf16x2_of_e4m3<false>(v2[e][1], 1.f), bf16x2_of_e4m3<true>(v2[e][1], 1.f)};
+      } else {
+        const int key = 4 * g4 + (n >> 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          at[e] = lds_address(
+              vst + key * ROWB +
+              (((2 * (d4 + e) + ((n >> 1) & 1)) ^ swizzle<ROWB>(key)) << 4) + 8 * (n & 1));
+        read_tr16<16 * ROWB>(at, vf);
       }
-      acc[dt] = mfma16(vf, pf, acc[dt]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[d4 + e] = mfma16(vf[e], pf, acc[d4 + e]);
     }
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // the stage has been read before it is written again
-    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  if (steps > 0) {
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u) issue(u, u, u == 0);
+    for (int i0 = 0; i0 < steps; i0 += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u;
+        // the stage to be filled was read by the step before: those reads are
+        // complete before loads may write it (a load to LDS is not ordered
+        // after earlier reads of its wave)
+        wait_lds();
+        // past the last step the loads have no rows left and read nothing:
+        // every step issues the same number
+        issue(i + U - 1, (u + U - 1) % U, false);
+        if (i < steps) {
+          wait_loads<HALF * 2 * (U - 1) + HALF>();
+          step(i, u);
+        }
+      }
+    }
   }
-  if (bad) l = NAN;
+  wait_loads<0>();
+  if (__ballot(bad)) l = NAN;
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
 
-  // Join of the four waves: [wave][row] m, l, then [wave][row][D] sums.
+  // Join of the waves: [wave][row] m, l, then [wave][row][D] sums.
   __syncthreads();
   float* ml = reinterpret_cast<float*>(smem);
   float* sums = ml + NW * R * 2;
@@ -250,7 +540,8 @@ __global__ __launch_bounds__(256) void attend_rows16_kernel(const AttnArgs a) {
   for (int dt = 0; dt < D / 16; ++dt)
     *reinterpret_cast<f32x4*>(sums + (wv * R + n) * D + dt * 16 + 4 * g4) = acc[dt];
   __syncthreads();
-  const int row = threadIdx.x >> 4;
+  constexpr int TPR = NW * 64 / R;          // threads a row
+  const int row = threadIdx.x / TPR;
   if (row >= t.rows) return;
   float top = -INFINITY;
 #pragma unroll
@@ -262,32 +553,72 @@ __global__ __launch_bounds__(256) void attend_rows16_kernel(const AttnArgs a) {
     f[w] = __builtin_amdgcn_exp2f(ml[(w * R + row) * 2] - ref);
     tot += f[w] * ml[(w * R + row) * 2 + 1];
   }
-  const float inv = tot == 0.f ? 0.f : 1.f / tot;  // a row that sees nothing gives zeros
+  const bool whole = it.pieces == 1;
+  const float inv = !whole ? 1.f : tot == 0.f ? 0.f : 1.f / tot;  // a row that sees nothing: zeros
   const int i = (t.row0 + row) / a.group;
-  uint16_t* o = a.out + ((int64_t)(t.first_q + i) * a.heads + head * a.group + (t.row0 + row) -
+  uint16_t* o = a.out + ((int64_t)(t.first_q + i) * a.heads + it.head * a.group + (t.row0 + row) -
                          i * a.group) * D;
+  const int item = (it.first + it.piece) * a.kv_heads + it.head;
+  if (!whole && threadIdx.x % TPR == 0) {
+    float* p = ml_at(a, c, D, item) + row * 2;
+    p[0] = top;
+    p[1] = tot;
+  }
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c) {
-    const int d0 = c * 64 + (threadIdx.x & 15) * 4;
+  for (int k = 0; k < D / (4 * TPR); ++k) {
+    const int d0 = (k * TPR + threadIdx.x % TPR) * 4;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < NW; ++w)
       v += f[w] * *reinterpret_cast<const f32x4*>(sums + (w * R + row) * D + d0);
     v *= inv;
-    *reinterpret_cast<u32x2*>(o + d0) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+    if (whole)
+      *reinterpret_cast<u32x2*>(o + d0) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+    else
+      *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + row * D + d0) = v;
   }
 }
 
+// Tiles of R rows that the call can have at most.
+int64_t most_tiles(const AttnArgs& a, int R) {
+  const int64_t all = (int64_t)a.tokens * a.group / R + a.seqs;
+  const int64_t by_seq = (int64_t)a.seqs * (((int64_t)a.max_q * a.group + R - 1) / R);
+  return all < by_seq ? all : by_seq;
+}
+
+Cut cut_of(const AttnArgs&) { return Cut{16, 1024, 4}; }
+
+// Items that the plan can have at most (and the grid).
+int64_t most_items(const AttnArgs& a, const Cut& c) {
+  return most_tiles(a, c.R) * a.kv_heads + c.target + 8;
+}
+
+// Whether a tile can be cut at all: blocks_of() past min_blocks.
+bool may_cut(const AttnArgs& a, const Cut& c) {
+  return ((int64_t)a.width * a.page + 31) / 32 + 1 > c.min_blocks;
+}
+
 template <int D, bool Q8>
-hipError_t run(const AttnArgs& a, hipStream_t s) {
-  const dim3 grid(a.kv_heads, (unsigned)(((int64_t)a.max_q * a.group + 15) / 16), a.seqs);
-  attend_rows16_kernel<D, Q8><<<grid, 256, 0, s>>>(a);
+hipError_t run(AttnArgs a, hipStream_t s) {
+  const Cut c = cut_of(a);
+  const bool cut = may_cut(a, c);
+  a.items = (int)(cut ? most_items(a, c) : most_tiles(a, c.R) * a.kv_heads);
+  constexpr int U = 2;
+  attend_rows16_kernel<D, Q8, 4, U><<<a.items, 256, 0, s>>>(a, c);
+  if (cut) {
+    const int64_t joins = most_tiles(a, c.R) * a.kv_heads * ((c.R + 3) / 4);
+    join_pieces_kernel<D><<<(unsigned)joins, 256, 0, s>>>(a, c);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t paged_attention_workspace(const AttnArgs&) { return 0; }
+size_t paged_attention_workspace(const AttnArgs& a) {
+  const Cut c = cut_of(a);
+  if (!may_cut(a, c)) return 0;
+  return (size_t)most_items(a, c) * c.R * (a.dim + 2) * sizeof(float);
+}
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t s) {
   const bool q8 = a.scale[0] != nullptr;

@@ -51,6 +51,7 @@ struct AttnArgs {
   int64_t pages;
   int tokens, seqs, max_q, heads, kv_heads, group, dim, page, width;
   int window;                // 0: none
+  int items;                 // pieces that the workspace has room for (set by the launcher)
   float scale_log2;          // softmax scale * log2(e)
 };
 size_t paged_attention_workspace(const AttnArgs& a);
