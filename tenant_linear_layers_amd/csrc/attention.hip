@@ -65,12 +65,16 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, int q0, int n, int le
   return x;
 }
 
-// LDS image of key/value rows: 16-byte pieces of a row permuted by the row
-// so that both readers below meet all the banks.
+// LDS image of key/value rows: the 16-byte pieces of a row are permuted (xor)
+// by a function of the row under which 8 rows in a row at one piece (a read of
+// K) and 4 rows at a pair of pieces (a transposing read of V) lie in different
+// banks: the bits of the row above those that change the bank line, rotated
+// left by one.
 template <int ROWB>
 __device__ __forceinline__ int swizzle(int key) {
   constexpr int P = ROWB / 16, KPL = ROWB >= 256 ? 1 : 256 / ROWB;
-  return (key / KPL) & (P - 1);
+  const int x = (key / KPL) & (P - 1);
+  return ((x << 1) | (x / (P / 2))) & (P - 1);
 }
 
 __device__ __forceinline__ float scale_of(uint32_t dword, int r) {
@@ -168,9 +172,11 @@ __device__ bool find_item(const AttnArgs& a, const Cut& c, int idx, Item& it) {
       it.n = __builtin_amdgcn_readlane(n, src);
       it.len = __builtin_amdgcn_readlane(len, src);
       const int local = want - __builtin_amdgcn_readlane(at, src);
-      it.tile = JOIN ? local : local / it.pieces;
-      it.piece = JOIN ? 0 : local - it.tile * it.pieces;
-      it.first = first + __builtin_amdgcn_readlane(isum - items, src) + it.tile * it.pieces;
+      // a sequence's last tiles see the most keys and come first
+      const int turn = JOIN ? local : local / it.pieces;
+      it.tile = tiles_of(a, c, it.n) - 1 - turn;
+      it.piece = JOIN ? 0 : local - turn * it.pieces;
+      it.first = first + __builtin_amdgcn_readlane(isum - items, src) + turn * it.pieces;
       return true;
     }
     before += __builtin_amdgcn_readlane(sum, 63);
@@ -267,6 +273,20 @@ __device__ __forceinline__ void read_tr16(const uint32_t (&at)[4], u32x4 (&v)[4]
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     v[i] = u32x4{r[2 * i][0], r[2 * i][1], r[2 * i + 1][0], r[2 * i + 1][1]};
+}
+
+// Two tiles of dims, at[2 d] and at[2 d + 1] the blocks of rows k and k + 8:
+// v[2 d + c] has the rows 16 c + k and 16 c + k + 8, OFF = 16 rows.
+template <int OFF>
+__device__ __forceinline__ void read_tr16_2x2(const uint32_t (&at)[4], u32x4 (&v)[4]) {
+  u32x4 r[4];
+  read_tr16<OFF>(at, r);
+#pragma unroll
+  for (int d = 0; d < 2; ++d)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      v[2 * d + c] = u32x4{r[2 * d][2 * c], r[2 * d][2 * c + 1], r[2 * d + 1][2 * c],
+                           r[2 * d + 1][2 * c + 1]};
 }
 
 __device__ __forceinline__ void read_tr8(const uint32_t (&at)[4], u32x2 (&r)[4]) {
@@ -579,6 +599,424 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
   }
 }
 
+// ------------------------------------------------------------------ many rows
+// Tiles of 64 RG rows.  A wave holds 64 rows (two column tiles of 32 queries,
+// so each operand read from LDS feeds two matrix products) and RG waves share
+// the staged keys; KG = 4 / RG such groups take the 32-key steps of the piece
+// in turn.  One wave a SIMD: 2 D registers of sums and D of queries a lane.
+//
+// The scores of step i + 1 are formed while the softmax of step i runs, so
+// that the matrix cores work under the exponentials: K is wanted one step
+// before V, and their two rings in LDS are NB steps deep each.
+//
+// bf16 rows go straight from memory to LDS.  e4m3 rows pass through registers
+// and are written as bf16, each times its scale (exact), so that the
+// conversion is made once for the workgroup and not by every wave.
+template <int D, bool Q8, int RG>
+struct Many {
+  static constexpr int KG = 4 / RG, R = 64 * RG;
+  static constexpr int NB = 2;
+  static constexpr int ROWB = 2 * D;                 // in LDS
+  static constexpr int STAGE = 32 * ROWB;            // 32 keys of K or V
+  static constexpr int RING = 2 * NB * STAGE;        // K's, then V's
+  static constexpr int SUMS = KG > 1 ? KG * R * (D + 2) * 4 : 0;
+  static constexpr int SMEM = KG * RING > SUMS ? KG * RING : SUMS;
+};
+
+template <int D, bool Q8, int RG>
+__global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, const Cut c) {
+  using M = Many<D, Q8, RG>;
+  constexpr int KG = M::KG, R = M::R, NB = M::NB, ROWB = M::ROWB, STAGE = M::STAGE;
+  constexpr int SRC = Q8 ? D : 2 * D;                // bytes of a row in memory
+  constexpr int P = SRC / 16;                        // its 16-byte pieces
+  constexpr int KPI = 64 / P;                        // keys per load of a wave
+  constexpr int LOADS = 32 / KPI;                    // loads per step of K, over RG waves
+  constexpr int MINE = (LOADS + RG - 1) / RG;        // at most, by one wave
+  __shared__ __attribute__((aligned(16))) char smem[M::SMEM];
+
+  Item it;
+  if (!find_item<false>(a, c, blockIdx.x, it)) return;
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rg = wv % RG, kg = wv / RG;
+  const int n = lane & 31, hh = lane >> 5;
+  const Tile t = tile_of(a, it.q0, it.n, it.len, it.tile, R);
+  int lo, hi;
+  piece_range(t, it.piece, it.pieces, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  const int kbeg = (lo & ~31) + 32 * kg;
+  const int steps = __builtin_amdgcn_readfirstlane(
+      hi > lo ? (hi - (lo & ~31) + 32 * KG - 1) / (32 * KG) : 0);   // of every group
+
+  // Q^T of the wave's rows and what each of them sees
+  u32x4 qf[2][D / 16];
+  int vis_hi[2], vis_lo[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int row = t.row0 + min(64 * rg + 32 * x + n, t.rows - 1);
+    const int qi = row / a.group;
+    const uint16_t* qp = a.q + (int64_t)(t.first_q + qi) * a.q_token_stride +
+                         (int64_t)(it.head * a.group + row - qi * a.group) * a.q_head_stride;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      qf[x][s] = *reinterpret_cast<const u32x4_any*>(qp + 16 * s + 8 * hh);
+    vis_hi[x] = min(t.pos0 + qi + 1, hi);
+    vis_lo[x] = a.window ? t.pos0 + qi - a.window + 1 : 0;
+  }
+  // the first and last query of the wave's rows: keys that all of them see
+  const int first_q = (t.row0 + min(64 * rg, t.rows - 1)) / a.group;
+  const int last_q = (t.row0 + min(64 * rg + 63, t.rows - 1)) / a.group;
+  const int all_hi = __builtin_amdgcn_readfirstlane(min(t.pos0 + first_q + 1, hi));
+  const int all_lo =
+      __builtin_amdgcn_readfirstlane(a.window ? t.pos0 + last_q - a.window + 1 : 0);
+
+  char* kring = smem + kg * M::RING;
+  char* vring = kring + NB * STAGE;
+  bool bad = false;
+  int blocks = -1;   // lane 2 i + h: rows / 16 of the cache for half h of step i (mod 32)
+
+  auto find_blocks = [&](int i) {
+    const int64_t key = (int64_t)kbeg + (int64_t)32 * KG * (i + (lane >> 1)) + 16 * (lane & 1);
+    blocks = -1;
+    if (key < hi) {
+      const int at = (int)key / a.page;
+      const int page = a.table[(int64_t)it.b * a.width + at];
+      if (page >= 0 && page < a.pages)
+        blocks =
+            (int)((((int64_t)page * a.kv_heads + it.head) * a.page + (key - at * a.page)) >> 4);
+      else  // a page that the cache lacks: the rows that see it are NaN
+        bad |= key + 16 > lo;
+    }
+  };
+  // rows / 16 and valid keys of both halves of step i
+  struct Rows {
+    int blk[2], keys[2], below;
+  };
+  auto rows_of = [&](int i) {
+    if ((i & 31) == 0) find_blocks(i);
+    Rows r;
+    const int key0 = kbeg + 32 * KG * i;
+    r.below = lo - key0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int blk = __builtin_amdgcn_readlane(blocks, 2 * (i & 31) + h);
+      r.keys[h] = __builtin_amdgcn_readfirstlane(
+          blk < 0 || i >= steps ? 0 : min(max(hi - key0 - 16 * h, 0), 16));
+      r.blk[h] = max(blk, 0);
+    }
+    return r;
+  };
+
+  // bf16: the wave's share of step i of K (w = 0) or V (1), straight into LDS
+  auto stage = [&](int w, int i, const Rows& r) {
+    char* st = (w ? vring : kring) + (i % NB) * STAGE;
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) {
+      const int load = rg + RG * j;                  // of the step's LOADS
+      const int h = load / (LOADS / 2);
+      const int key = (load % (LOADS / 2)) * KPI + lane / P;   // of the half
+      const int off = key * SRC + (((lane % P) ^ swizzle<ROWB>(key)) << 4);
+      lds_bload16(a.cache[w] + (int64_t)(h ? r.blk[1] : r.blk[0]) * (16 * SRC),
+                  (h ? r.keys[1] : r.keys[0]) * SRC, 16 * h + key < r.below ? 1 << 30 : off, 0,
+                  st + load * 1024);
+    }
+  };
+  // e4m3: the same rows and their scales into registers, then as bf16 into LDS
+  u32x4 raw[2][MINE];
+  uint32_t sc[2][MINE];
+  auto fetch = [&](int w, const Rows& r) {
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) {
+      const int load = rg + RG * j;
+      if (LOADS % RG != 0 && load >= LOADS) break;
+      const int h = load / (LOADS / 2);
+      const int key = (load % (LOADS / 2)) * KPI + lane / P;
+      const bool below = 16 * h + key < r.below;
+      const int blk = h ? r.blk[1] : r.blk[0], keys = h ? r.keys[1] : r.keys[0];
+      raw[w][j] = bload128(a.cache[w] + (int64_t)blk * (16 * SRC), keys * SRC,
+                           below ? 1 << 30 : key * SRC + (lane % P) * 16, 0);
+      sc[w][j] = bload8(a.scale[w] + (int64_t)blk * 16, keys, below ? 1 << 30 : key, 0);
+    }
+  };
+  auto put = [&](int w, int i) {
+    char* st = (w ? vring : kring) + (i % NB) * STAGE;
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) {
+      const int load = rg + RG * j;
+      if (LOADS % RG != 0 && load >= LOADS) break;
+      const int key = load * KPI + lane / P;          // of the step
+      const float s = __uint_as_float(sc[w][j] << 23);
+      const u32x4 r = raw[w][j];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int piece = 2 * (lane % P) + e;
+        *reinterpret_cast<u32x4*>(st + key * ROWB + ((piece ^ swizzle<ROWB>(key)) << 4)) =
+            u32x4{bf16x2_of_e4m3<false>(r[2 * e], s), bf16x2_of_e4m3<true>(r[2 * e], s),
+                  bf16x2_of_e4m3<false>(r[2 * e + 1], s), bf16x2_of_e4m3<true>(r[2 * e + 1], s)};
+      }
+    }
+  };
+
+  f32x16 acc[2][D / 32];
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[x][d][r] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  auto zero = [](f32x16 (&z)[2]) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) z[x][r] = 0.f;
+  };
+  // one sixteen of the dims of the scores of step i
+  auto score = [&](int i, int s, f32x16 (&z)[2]) {
+    const u32x4 k4 = *reinterpret_cast<const u32x4*>(
+        kring + (i % NB) * STAGE + n * ROWB + (((2 * s + hh) ^ swizzle<ROWB>(n)) << 4));
+    z[0] = mfma32(k4, qf[0][s], z[0]);
+    z[1] = mfma32(k4, qf[1][s], z[1]);
+  };
+
+  // Masks the scores of step i and moves the references.
+  auto look = [&](int i, f32x16 (&z)[2]) {
+    const int key0 = kbeg + 32 * KG * i;
+    const bool masked = key0 + 32 > all_hi || key0 < all_lo;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int j = key0 + 8 * (r >> 2) + 4 * hh + (r & 3);
+          z[x][r] = j < vis_hi[x] && j >= vis_lo[x] ? z[x][r] : -INFINITY;
+        }
+      }
+      float top = z[x][0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) top = fmaxf(top, z[x][r]);
+      top *= a.scale_log2;
+      // only when a score passes the reference by 2^6: see above
+      if (__ballot(top > m[x] + 6.f)) {
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m1 = fmaxf(m[x], top);
+        const float f = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[x] - m1);
+        m[x] = m1;
+        l[x] *= f;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) acc[x][d] *= f;
+      }
+    }
+  };
+
+  // Two scores of column tile x to packed weights: pf[x][c] holds the keys
+  // 16 c + 8 (j / 4) + 4 hh + j % 4 of the step.
+  auto weigh = [&](int x, int r, const float (&ref)[2], f32x16 (&z)[2], u32x4 (&pf)[2][2]) {
+    const float p0 = __builtin_amdgcn_exp2f(fmaf(z[x][r], a.scale_log2, -ref[x]));
+    const float p1 = __builtin_amdgcn_exp2f(fmaf(z[x][r + 1], a.scale_log2, -ref[x]));
+    l[x] += p0;
+    l[x] += p1;
+    pf[x][r >> 3][(r & 7) >> 1] = cvt_pk_bf16(p0, p1);
+  };
+
+  // V^T: lane (dim, hh) of tile d wants the rows 16 c + 4 hh + 0..3 and those
+  // + 8; its 16 lanes read them at 4 rows x 32 bytes
+  int voff[D / 32][2];
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int k = 8 * e + 4 * hh + ((lane & 15) >> 2);
+      const int piece = 4 * d + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+      voff[d][e] = k * ROWB + ((piece ^ swizzle<ROWB>(k)) << 4) + 8 * (lane & 1);
+    }
+  auto values = [&](int i, const u32x4 (&pf)[2][2]) {
+    const uint32_t st = lds_address(vring + (i % NB) * STAGE);
+#pragma unroll
+    for (int d = 0; d < D / 32; d += 2) {
+      u32x4 vf[4];
+      const uint32_t at[4] = {st + voff[d][0], st + voff[d][1], st + voff[d + 1][0],
+                              st + voff[d + 1][1]};
+      read_tr16_2x2<16 * ROWB>(at, vf);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            acc[x][d + e] = mfma32(vf[2 * e + k], pf[x][k], acc[x][d + e]);
+    }
+  };
+
+  auto meet = [&]() {   // the group's waves: stages written, or read to the end
+    if (RG > 1) asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  if (steps > 0) {
+    f32x16 z[2];
+    Rows last;   // of the step that V is staged next
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {   // K of steps 0 .. NB - 1, V of 0 .. NB - 2
+      last = rows_of(i);
+      if (Q8) {
+        fetch(0, last);
+        put(0, i);
+      } else {
+        stage(0, i, last);
+      }
+      if (i == NB - 1) break;
+      if (Q8) {
+        fetch(1, last);
+        put(1, i);
+      } else {
+        stage(1, i, last);
+      }
+    }
+    if (Q8) {
+      fetch(1, last);
+      last = rows_of(NB);
+      fetch(0, last);
+    } else {
+      wait_loads<0>();
+    }
+    wait_lds();
+    meet();
+    zero(z);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) score(0, s, z);
+    for (int i = 0; i < steps; ++i) {
+      // K of step i + 1 and V of step i have arrived, and all waves have the
+      // scores of step i and the values of step i - 1 behind them: K's stage
+      // i and V's stage i - 1 may be written.
+      if (!Q8) wait_loads<(NB - 2) * 2 * MINE>();
+      wait_lds();
+      meet();
+      if (Q8) {
+        put(0, i + NB);
+        put(1, i + NB - 1);
+        fetch(1, last);
+        last = rows_of(i + NB + 1);
+        fetch(0, last);
+      } else {
+        stage(1, i + NB - 1, last);
+        last = rows_of(i + NB);
+        stage(0, i + NB, last);
+      }
+      look(i, z);
+      const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+      f32x16 next[2];
+      u32x4 pf[2][2];
+      zero(next);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        score(i + 1, s, next);
+#pragma unroll
+        for (int e = 0; e < 256 / D; ++e) {
+          const int w = s * (256 / D) + e;   // 16 pairs: 8 of each column tile
+          weigh(w >> 3, 2 * (w & 7), ref, z, pf);
+        }
+      }
+      values(i, pf);
+      z[0] = next[0];
+      z[1] = next[1];
+    }
+  }
+  wait_loads<0>();
+  wait_lds();
+  const bool nan = __ballot(bad) != 0;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    if (nan) l[x] = NAN;
+    l[x] += __shfl_xor(l[x], 32);
+  }
+
+  const bool whole = it.pieces == 1;
+  const int item = (it.first + it.piece) * a.kv_heads + it.head;
+  if (KG == 1) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = 64 * rg + 32 * x + n;
+      if (row >= t.rows) continue;
+      const int qi = (t.row0 + row) / a.group;
+      uint16_t* o = a.out + ((int64_t)(t.first_q + qi) * a.heads + it.head * a.group +
+                             (t.row0 + row) - qi * a.group) * D;
+      const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];   // a row that sees nothing: zeros
+      if (!whole && hh == 0) {
+        float* p = ml_at(a, c, D, item) + row * 2;
+        p[0] = m[x];
+        p[1] = l[x];
+      }
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 v = {acc[x][d][4 * r], acc[x][d][4 * r + 1], acc[x][d][4 * r + 2],
+                           acc[x][d][4 * r + 3]};
+          const int d0 = 32 * d + 8 * r + 4 * hh;
+          if (whole)
+            *reinterpret_cast<u32x2*>(o + d0) =
+                u32x2{cvt_pk_bf16(v[0] * inv, v[1] * inv), cvt_pk_bf16(v[2] * inv, v[3] * inv)};
+          else
+            *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + (size_t)row * D + d0) = v;
+        }
+    }
+    return;
+  }
+  // Join of the groups: [group][row] m, l, then [group][row][D] sums.
+  __syncthreads();
+  float* ml = reinterpret_cast<float*>(smem);
+  float* sums = ml + KG * R * 2;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int at = kg * R + 64 * rg + 32 * x + n;
+    if (hh == 0) {
+      ml[at * 2] = m[x];
+      ml[at * 2 + 1] = l[x];
+    }
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<f32x4*>(sums + at * D + 32 * d + 8 * r + 4 * hh) =
+            f32x4{acc[x][d][4 * r], acc[x][d][4 * r + 1], acc[x][d][4 * r + 2],
+                  acc[x][d][4 * r + 3]};
+  }
+  __syncthreads();
+  constexpr int TPR = D / 4, RPP = 256 / TPR;   // threads a row, rows a pass
+  for (int row = threadIdx.x / TPR; row < t.rows; row += RPP) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < KG; ++w) top = fmaxf(top, ml[(w * R + row) * 2]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const int d0 = (threadIdx.x % TPR) * 4;
+    float tot = 0.f;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < KG; ++w) {
+      const float f = __builtin_amdgcn_exp2f(ml[(w * R + row) * 2] - ref);
+      tot += f * ml[(w * R + row) * 2 + 1];
+      v += f * *reinterpret_cast<const f32x4*>(sums + (w * R + row) * D + d0);
+    }
+    if (whole) {
+      v *= tot == 0.f ? 0.f : 1.f / tot;
+      const int qi = (t.row0 + row) / a.group;
+      uint16_t* o = a.out + ((int64_t)(t.first_q + qi) * a.heads + it.head * a.group +
+                             (t.row0 + row) - qi * a.group) * D;
+      *reinterpret_cast<u32x2*>(o + d0) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+    } else {
+      *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + (size_t)row * D + d0) = v;
+      if (d0 == 0) {
+        float* p = ml_at(a, c, D, item) + row * 2;
+        p[0] = top;
+        p[1] = tot;
+      }
+    }
+  }
+}
+
 // Tiles of R rows that the call can have at most.
 int64_t most_tiles(const AttnArgs& a, int R) {
   const int64_t all = (int64_t)a.tokens * a.group / R + a.seqs;
@@ -586,7 +1024,16 @@ int64_t most_tiles(const AttnArgs& a, int R) {
   return all < by_seq ? all : by_seq;
 }
 
-Cut cut_of(const AttnArgs&) { return Cut{16, 1024, 4}; }
+// Rows a tile: 16 for tokens by themselves, otherwise 64 RG.  See run().
+int rows_per_tile(const AttnArgs& a) {
+  if ((int64_t)a.max_q * a.group <= 16) return 16;
+  return (int64_t)a.tokens * a.group / 256 * a.kv_heads >= 128 ? 256 : 64;
+}
+
+Cut cut_of(const AttnArgs& a) {
+  const int R = rows_per_tile(a);
+  return R == 16 ? Cut{R, 1024, 4} : Cut{R, 256, 16};
+}
 
 // Items that the plan can have at most (and the grid).
 int64_t most_items(const AttnArgs& a, const Cut& c) {
@@ -603,8 +1050,12 @@ hipError_t run(AttnArgs a, hipStream_t s) {
   const Cut c = cut_of(a);
   const bool cut = may_cut(a, c);
   a.items = (int)(cut ? most_items(a, c) : most_tiles(a, c.R) * a.kv_heads);
-  constexpr int U = 2;
-  attend_rows16_kernel<D, Q8, 4, U><<<a.items, 256, 0, s>>>(a, c);
+  if (c.R == 16)
+    attend_rows16_kernel<D, Q8, 4, 2><<<a.items, 256, 0, s>>>(a, c);
+  else if (c.R == 64)
+    attend_many_kernel<D, Q8, 1><<<a.items, 256, 0, s>>>(a, c);
+  else
+    attend_many_kernel<D, Q8, 4><<<a.items, 256, 0, s>>>(a, c);
   if (cut) {
     const int64_t joins = most_tiles(a, c.R) * a.kv_heads * ((c.R + 3) / 4);
     join_pieces_kernel<D><<<(unsigned)joins, 256, 0, s>>>(a, c);
