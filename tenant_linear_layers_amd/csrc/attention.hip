@@ -56,7 +56,7 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, int q0, int n, int le
   x.row0 = t * R;
   x.rows = min(R, n * a.group - x.row0);
   x.pos0 = len - n;
-  const int i0 = x.row0 / a.group, i1 = (x.row0 + x.rows - 1) / a.group;
+  const int i0 = a.by_group.of(x.row0), i1 = a.by_group.of(x.row0 + x.rows - 1);
   x.hi = max(min(len, x.pos0 + i1 + 1), 0);
   x.lo = a.window ? max(x.pos0 + i0 - a.window + 1, 0) : 0;
   x.all_hi = x.pos0 + i0 + 1;
@@ -86,12 +86,16 @@ __device__ __forceinline__ float scale_of(uint32_t dword, int r) {
 // index -> (sequence b, tile, piece of the tile's keys, key/value head), heads
 // fastest, pieces next.  A sequence whose widest tile has `blocks` blocks of
 // 32 keys is cut into ceil(blocks / C) pieces a tile, with C such that all
-// items together are about `target`; each piece takes an equal share of its
+// items together are about `round` or `target`; each piece takes an equal share of its
 // own tile's blocks.  Then items <= target + tiles * kv_heads, which bounds
 // the grid and the workspace on the host.  Every wave computes the same plan
 // (lane by sequence, 64 at a time), and the joining kernel again.
 struct Cut {
-  int R, target, min_blocks;   // rows a tile, items aimed at, blocks a piece at least
+  int R;                       // rows a tile
+  int round, target;           // items of one round of the card; items aimed at
+  int min_blocks, enough;      // blocks a piece: at least; for more than one round
+  int least, most;             // rows (n * group) of the sequences taken: least < rows <= most
+  float share;                 // kv_heads / round; 0: nothing is cut
 };
 
 struct Item {
@@ -100,87 +104,88 @@ struct Item {
   int first;                   // index of the tile's first piece, by head
 };
 
-__device__ __forceinline__ int blocks_of(const AttnArgs& a, const Cut& c, int n, int len) {
-  const int qs = min(n, c.R / a.group + 2);                 // queries that a tile can hold rows of
-  const int64_t keys = a.window ? min((int64_t)len, (int64_t)a.window + qs) : len;
-  return (int)((keys + 31) >> 5) + (a.window ? 1 : 0);
-}
+// One sequence's part of the plan.
+struct Seq {
+  int q0, n, len, tiles, blocks;
+};
 
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, const Cut& c, int n) {
-  return (n * a.group + c.R - 1) / c.R;
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, const Cut& c, int b) {
+  Seq s;
+  seq_range(a, b, s.q0, s.n, s.len);
+  const int rows = s.n * a.group;
+  s.tiles = rows > c.least && rows <= c.most ? (rows + c.R - 1) / c.R : 0;  // R: a power of two
+  const uint32_t span = (uint32_t)a.window + (uint32_t)min(s.n, c.R);   // keys a tile can see
+  const uint32_t keys = a.window ? min((uint32_t)s.len, span) : (uint32_t)s.len;
+  s.blocks = (int)((keys + 31) >> 5) + (a.window ? 1 : 0);
+  return s;
 }
 
 // Item idx (JOIN: tile idx, its first piece); false past the last one.
 template <bool JOIN>
-__device__ bool find_item(const AttnArgs& a, const Cut& c, int idx, Item& it) {
+__device__ __forceinline__ bool find_item(const AttnArgs& a, const Cut& c, int idx, Item& it) {
   const int lane = threadIdx.x & 63;
-  it.head = idx % a.kv_heads;
-  const int want = idx / a.kv_heads;
+  const int want = a.by_heads.of(idx);
+  it.head = __builtin_amdgcn_readfirstlane(idx - want * a.kv_heads);
+  const bool many = a.seqs > 64;
+  Seq s{};
   float load = 0.f;
-  int q0 = 0, n = 0, len = 0, tiles = 0, blocks = 0;
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
     float mine = 0.f;
     if (b0 + lane < a.seqs) {
-      seq_range(a, b0 + lane, q0, n, len);
-      tiles = tiles_of(a, c, n);
-      blocks = blocks_of(a, c, n, len);
-      mine = (float)tiles * (float)blocks;
+      s = seq_of(a, c, b0 + lane);
+      mine = (float)s.tiles * (float)s.blocks;
     }
-    if (a.seqs == 1) {
-      load = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(mine)));
-    } else {
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(mine, o);
-      load += mine;
-    }
+    if (c.share == 0.f) break;
+#pragma unroll 1
+    for (int o = a.seqs > 1 ? 32 : 0; o > 0; o >>= 1) mine += __shfl_xor(mine, o);
+    load += __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(mine)));
   }
-  const int C = max((int)fminf(load * (float)a.kv_heads / (float)c.target, 1e9f) + 1, c.min_blocks);
-  int before = 0, first = 0;   // tiles (JOIN) or items before this chunk; items before it
+  // One round of the card for little work, four for more: their ends differ by
+  // a piece, and a longer piece has its start and end to set against.
+  const float one = load * c.share, four = one * ((float)c.round / (float)c.target);
+  const float C = fmaxf(floorf(fmaxf(fminf(one, (float)c.enough), four)) + 1.f,
+                        (float)c.min_blocks);
+  const float per_C = 1.f / C;
+  int before = 0, first = 0;   // tiles (JOIN) or items of the chunks before; items of them
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
-    int pieces = 1, items = 0, at = 0, tl = 0;
+    int pieces = 1, items = 0, tl = 0;
     if (b0 + lane < a.seqs) {
-      if (a.seqs > 64) {
-        seq_range(a, b0 + lane, q0, n, len);
-        tiles = tiles_of(a, c, n);
-        blocks = blocks_of(a, c, n, len);
-      }
-      pieces = max((blocks + C - 1) / C, 1);
-      items = tiles * pieces;
-      tl = tiles;
+      if (many) s = seq_of(a, c, b0 + lane);
+      if (c.share != 0.f) pieces = max((int)((float)(s.blocks - 1) * per_C) + 1, 1);
+      items = s.tiles * pieces;
+      tl = s.tiles;
     }
     int sum = JOIN ? tl : items, isum = items;
-    if (a.seqs > 1) {
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int up = __shfl_up(sum, o), iup = JOIN ? __shfl_up(isum, o) : 0;
-        if (lane >= o) {
-          sum += up;
-          isum += iup;
-        }
+#pragma unroll 1
+    for (int o = 1; o < min(a.seqs, 64); o <<= 1) {
+      const int up = __shfl_up(sum, o), iup = JOIN ? __shfl_up(isum, o) : 0;
+      if (lane >= o) {
+        sum += up;
+        isum += iup;
       }
     }
     if (!JOIN) isum = sum;
     const int width = JOIN ? tl : items;
-    at = before + sum - width;
+    const int at = before + sum - width;
     const uint64_t hit = __ballot(want >= at && want < at + width);
     if (hit) {
       const int src = __builtin_ctzll(hit);
       it.b = b0 + src;
-      it.head = __builtin_amdgcn_readfirstlane(it.head);
       it.pieces = __builtin_amdgcn_readlane(pieces, src);
-      it.q0 = __builtin_amdgcn_readlane(q0, src);
-      it.n = __builtin_amdgcn_readlane(n, src);
-      it.len = __builtin_amdgcn_readlane(len, src);
+      it.q0 = __builtin_amdgcn_readlane(s.q0, src);
+      it.n = __builtin_amdgcn_readlane(s.n, src);
+      it.len = __builtin_amdgcn_readlane(s.len, src);
       const int local = want - __builtin_amdgcn_readlane(at, src);
       // a sequence's last tiles see the most keys and come first
-      const int turn = JOIN ? local : local / it.pieces;
-      it.tile = tiles_of(a, c, it.n) - 1 - turn;
+      const int turn = JOIN || it.pieces == 1 ? local : local / it.pieces;
+      it.tile = __builtin_amdgcn_readlane(s.tiles, src) - 1 - turn;
       it.piece = JOIN ? 0 : local - turn * it.pieces;
       it.first = first + __builtin_amdgcn_readlane(isum - items, src) + turn * it.pieces;
       return true;
     }
-    before += __builtin_amdgcn_readlane(sum, 63);
-    first += __builtin_amdgcn_readlane(isum, 63);
+    const int last = min(a.seqs, 64) - 1;
+    before += __builtin_amdgcn_readlane(sum, last);
+    first += __builtin_amdgcn_readlane(isum, last);
   }
   return false;
 }
@@ -188,10 +193,15 @@ __device__ bool find_item(const AttnArgs& a, const Cut& c, int idx, Item& it) {
 // Keys [lo, hi) of a piece: its share of the tile's blocks of 32.
 __device__ __forceinline__ void piece_range(const Tile& t, int piece, int pieces, int& lo,
                                             int& hi) {
+  lo = t.lo;
+  hi = t.hi;
+  if (pieces == 1) return;
   const int b0 = t.lo >> 5, nb = t.hi > t.lo ? ((t.hi + 31) >> 5) - b0 : 0;
-  lo = max((b0 + (int)((int64_t)nb * piece / pieces)) << 5, t.lo);
-  hi = min((b0 + (int)((int64_t)nb * (piece + 1) / pieces)) << 5, t.hi);
-  if (nb == 0) lo = hi = 0;
+  const int each = (nb + pieces - 1) / pieces;
+  const int from = min(each * piece, nb), to = min(from + each, nb);
+  lo = max((b0 + from) << 5, t.lo);
+  hi = min((b0 + to) << 5, t.hi);
+  if (from == to) lo = hi = 0;
 }
 
 // Sums of the pieces: [item][R][D] floats, then [item][R] (m, l).
@@ -202,45 +212,49 @@ __device__ __forceinline__ float* ml_at(const AttnArgs& a, const Cut& c, int D, 
   return a.partial + (size_t)a.items * c.R * D + (size_t)item * c.R * 2;
 }
 
-// One wave a row: the row's pieces added up, in the order of their keys.
+// One wave a row: the row's pieces added up, in the order of their keys.  A
+// workgroup takes 16 rows of a tile and head (4 of the tiles of 16).
 template <int D>
 __global__ __launch_bounds__(256) void join_pieces_kernel(const AttnArgs a, const Cut c) {
-  const int per = (c.R + 3) / 4;
+  const int rows = c.R == 16 ? 4 : 16, per = c.R / rows;   // powers of two
   Item it;
   if (!find_item<true>(a, c, blockIdx.x / per, it) || it.pieces == 1) return;
   // cu_q that does not rise could ask for more items than there are
   if ((it.first + it.pieces) * a.kv_heads > a.items) return;
   const int lane = threadIdx.x & 63;
-  const int row = (blockIdx.x % per) * 4 + (threadIdx.x >> 6);
-  const int r = it.tile * c.R + row;
-  if (row >= c.R || r >= it.n * a.group) return;
   const int item0 = it.first * a.kv_heads + it.head;
-  float top = -INFINITY;
-  for (int p = lane; p < it.pieces; p += 64)
-    top = fmaxf(top, ml_at(a, c, D, item0 + p * a.kv_heads)[row * 2]);
+  for (int k = threadIdx.x >> 6; k < rows; k += 4) {
+    const int row = (blockIdx.x & (per - 1)) * rows + k;
+    const int r = it.tile * c.R + row;
+    if (r >= it.n * a.group) return;
+    float top = -INFINITY;
+    for (int p = lane; p < it.pieces; p += 64)
+      top = fmaxf(top, ml_at(a, c, D, item0 + p * a.kv_heads)[row * 2]);
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  const float ref = top == -INFINITY ? 0.f : top;
-  constexpr int N = D / 64;
-  float tot = 0.f, v[N];
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    constexpr int N = D / 64;
+    float tot = 0.f, v[N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) v[e] = 0.f;
+    for (int e = 0; e < N; ++e) v[e] = 0.f;
 #pragma unroll 8
-  for (int p = 0; p < it.pieces; ++p) {
-    const int item = item0 + p * a.kv_heads;
-    const float* ml = ml_at(a, c, D, item) + row * 2;
-    const float f = __builtin_amdgcn_exp2f(ml[0] - ref);
-    tot = fmaf(f, ml[1], tot);
-    const float* s = sums_at(a, c, D, item) + (size_t)row * D + lane * N;
+    for (int p = 0; p < it.pieces; ++p) {
+      const int item = item0 + p * a.kv_heads;
+      const float* ml = ml_at(a, c, D, item) + row * 2;
+      const float f = __builtin_amdgcn_exp2f(ml[0] - ref);
+      tot = fmaf(f, ml[1], tot);
+      const float* s = sums_at(a, c, D, item) + (size_t)row * D + lane * N;
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = fmaf(f, s[e], v[e]);
+      for (int e = 0; e < N; ++e) v[e] = fmaf(f, s[e], v[e]);
+    }
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
+    const int i = a.by_group.of(r);
+    uint16_t* o =
+        a.out + ((int64_t)(it.q0 + i) * a.heads + it.head * a.group + r - i * a.group) * D +
+        lane * N;
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = f32_to_bf16_bits(v[e] * inv);
   }
-  const float inv = tot == 0.f ? 0.f : 1.f / tot;
-  const int i = r / a.group;
-  uint16_t* o = a.out + ((int64_t)(it.q0 + i) * a.heads + it.head * a.group + r - i * a.group) * D +
-                lane * N;
-#pragma unroll
-  for (int e = 0; e < N; ++e) o[e] = f32_to_bf16_bits(v[e] * inv);
 }
 
 // ------------------------------------------------------------------ reads of V
@@ -347,7 +361,7 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
   // Q^T: lane n's row, the dims that the lane's K pieces hold.
   u32x4 qf[D / 32];
   const int my = min(n, t.rows - 1);
-  const int qi = (t.row0 + my) / a.group;
+  const int qi = a.by_group.of(t.row0 + my);
   const uint16_t* qp =
       a.q + (int64_t)(t.first_q + qi) * a.q_token_stride +
       (int64_t)(it.head * a.group + (t.row0 + my) - qi * a.group) * a.q_head_stride;
@@ -375,7 +389,7 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
       const int64_t key = (int64_t)kbeg + (int64_t)32 * NW * (i + (lane >> 1)) + 16 * (lane & 1);
       blocks = -1;
       if (key < hi) {
-        const int at = (int)key / a.page;
+        const int at = a.by_page.of((int)key);
         const int page = a.table[(int64_t)it.b * a.width + at];
         if (page >= 0 && page < a.pages)
           blocks = (int)((((int64_t)page * a.kv_heads + it.head) * a.page + (key - at * a.page)) >>
@@ -575,7 +589,7 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
   }
   const bool whole = it.pieces == 1;
   const float inv = !whole ? 1.f : tot == 0.f ? 0.f : 1.f / tot;  // a row that sees nothing: zeros
-  const int i = (t.row0 + row) / a.group;
+  const int i = a.by_group.of(t.row0 + row);
   uint16_t* o = a.out + ((int64_t)(t.first_q + i) * a.heads + it.head * a.group + (t.row0 + row) -
                          i * a.group) * D;
   const int item = (it.first + it.piece) * a.kv_heads + it.head;
@@ -600,10 +614,9 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
 }
 
 // ------------------------------------------------------------------ many rows
-// Tiles of 64 RG rows.  A wave holds 64 rows (two column tiles of 32 queries,
-// so each operand read from LDS feeds two matrix products) and RG waves share
-// the staged keys; KG = 4 / RG such groups take the 32-key steps of the piece
-// in turn.  One wave a SIMD: 2 D registers of sums and D of queries a lane.
+// Tiles of 32 RG rows.  A wave holds 32 rows and RG waves share the staged
+// keys; KG = 4 / RG such groups take the 32-key steps of the piece in turn.
+// Two workgroups a CU: one's matrix products run under the other's softmax.
 //
 // The scores of step i + 1 are formed while the softmax of step i runs, so
 // that the matrix cores work under the exponentials: K is wanted one step
@@ -614,8 +627,8 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
 // conversion is made once for the workgroup and not by every wave.
 template <int D, bool Q8, int RG>
 struct Many {
-  static constexpr int KG = 4 / RG, R = 64 * RG;
-  static constexpr int NB = 2;
+  static constexpr int KG = 4 / RG, R = 32 * RG;
+  static constexpr int NB = Q8 || RG == 2 ? 2 : 4;
   static constexpr int ROWB = 2 * D;                 // in LDS
   static constexpr int STAGE = 32 * ROWB;            // 32 keys of K or V
   static constexpr int RING = 2 * NB * STAGE;        // K's, then V's
@@ -624,7 +637,7 @@ struct Many {
 };
 
 template <int D, bool Q8, int RG>
-__global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, const Cut c) {
+__global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, const Cut c) {
   using M = Many<D, Q8, RG>;
   constexpr int KG = M::KG, R = M::R, NB = M::NB, ROWB = M::ROWB, STAGE = M::STAGE;
   constexpr int SRC = Q8 ? D : 2 * D;                // bytes of a row in memory
@@ -650,23 +663,19 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, c
       hi > lo ? (hi - (lo & ~31) + 32 * KG - 1) / (32 * KG) : 0);   // of every group
 
   // Q^T of the wave's rows and what each of them sees
-  u32x4 qf[2][D / 16];
-  int vis_hi[2], vis_lo[2];
+  u32x4 qf[D / 16];
+  const int my = t.row0 + min(32 * rg + n, t.rows - 1);
+  const int qi = a.by_group.of(my);
+  const uint16_t* qp = a.q + (int64_t)(t.first_q + qi) * a.q_token_stride +
+                       (int64_t)(it.head * a.group + my - qi * a.group) * a.q_head_stride;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int row = t.row0 + min(64 * rg + 32 * x + n, t.rows - 1);
-    const int qi = row / a.group;
-    const uint16_t* qp = a.q + (int64_t)(t.first_q + qi) * a.q_token_stride +
-                         (int64_t)(it.head * a.group + row - qi * a.group) * a.q_head_stride;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      qf[x][s] = *reinterpret_cast<const u32x4_any*>(qp + 16 * s + 8 * hh);
-    vis_hi[x] = min(t.pos0 + qi + 1, hi);
-    vis_lo[x] = a.window ? t.pos0 + qi - a.window + 1 : 0;
-  }
+  for (int s = 0; s < D / 16; ++s)
+    qf[s] = *reinterpret_cast<const u32x4_any*>(qp + 16 * s + 8 * hh);
+  const int vis_hi = min(t.pos0 + qi + 1, hi);
+  const int vis_lo = a.window ? t.pos0 + qi - a.window + 1 : 0;
   // the first and last query of the wave's rows: keys that all of them see
-  const int first_q = (t.row0 + min(64 * rg, t.rows - 1)) / a.group;
-  const int last_q = (t.row0 + min(64 * rg + 63, t.rows - 1)) / a.group;
+  const int first_q = a.by_group.of(t.row0 + min(32 * rg, t.rows - 1));
+  const int last_q = a.by_group.of(t.row0 + min(32 * rg + 31, t.rows - 1));
   const int all_hi = __builtin_amdgcn_readfirstlane(min(t.pos0 + first_q + 1, hi));
   const int all_lo =
       __builtin_amdgcn_readfirstlane(a.window ? t.pos0 + last_q - a.window + 1 : 0);
@@ -680,7 +689,7 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, c
     const int64_t key = (int64_t)kbeg + (int64_t)32 * KG * (i + (lane >> 1)) + 16 * (lane & 1);
     blocks = -1;
     if (key < hi) {
-      const int at = (int)key / a.page;
+      const int at = a.by_page.of((int)key);
       const int page = a.table[(int64_t)it.b * a.width + at];
       if (page >= 0 && page < a.pages)
         blocks =
@@ -758,67 +767,54 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, c
     }
   };
 
-  f32x16 acc[2][D / 32];
+  f32x16 acc[D / 32];
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+  for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[x][d][r] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int r = 0; r < 16; ++r) acc[d][r] = 0.f;
+  float m = -INFINITY, l = 0.f;
 
-  auto zero = [](f32x16 (&z)[2]) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) z[x][r] = 0.f;
-  };
   // one sixteen of the dims of the scores of step i
-  auto score = [&](int i, int s, f32x16 (&z)[2]) {
+  auto score = [&](int i, int s, f32x16& z) {
     const u32x4 k4 = *reinterpret_cast<const u32x4*>(
         kring + (i % NB) * STAGE + n * ROWB + (((2 * s + hh) ^ swizzle<ROWB>(n)) << 4));
-    z[0] = mfma32(k4, qf[0][s], z[0]);
-    z[1] = mfma32(k4, qf[1][s], z[1]);
+    z = mfma32(k4, qf[s], z);
   };
 
   // Masks the scores of step i and moves the references.
-  auto look = [&](int i, f32x16 (&z)[2]) {
+  auto look = [&](int i, f32x16& z) {
     const int key0 = kbeg + 32 * KG * i;
-    const bool masked = key0 + 32 > all_hi || key0 < all_lo;
+    if (key0 + 32 > all_hi || key0 < all_lo) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (masked) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int j = key0 + 8 * (r >> 2) + 4 * hh + (r & 3);
-          z[x][r] = j < vis_hi[x] && j >= vis_lo[x] ? z[x][r] : -INFINITY;
-        }
+      for (int r = 0; r < 16; ++r) {
+        const int j = key0 + 8 * (r >> 2) + 4 * hh + (r & 3);
+        z[r] = j < vis_hi && j >= vis_lo ? z[r] : -INFINITY;
       }
-      float top = z[x][0];
+    }
+    float top = z[0];
 #pragma unroll
-      for (int r = 1; r < 16; ++r) top = fmaxf(top, z[x][r]);
-      top *= a.scale_log2;
-      // only when a score passes the reference by 2^6: see above
-      if (__ballot(top > m[x] + 6.f)) {
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m1 = fmaxf(m[x], top);
-        const float f = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[x] - m1);
-        m[x] = m1;
-        l[x] *= f;
+    for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
+    top *= a.scale_log2;
+    // only when a score passes the reference by 2^6: see above
+    if (__ballot(top > m + 6.f)) {
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m1 = fmaxf(m, top);
+      const float f = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m1);
+      m = m1;
+      l *= f;
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) acc[x][d] *= f;
-      }
+      for (int d = 0; d < D / 32; ++d) acc[d] *= f;
     }
   };
 
-  // Two scores of column tile x to packed weights: pf[x][c] holds the keys
-  // 16 c + 8 (j / 4) + 4 hh + j % 4 of the step.
-  auto weigh = [&](int x, int r, const float (&ref)[2], f32x16 (&z)[2], u32x4 (&pf)[2][2]) {
-    const float p0 = __builtin_amdgcn_exp2f(fmaf(z[x][r], a.scale_log2, -ref[x]));
-    const float p1 = __builtin_amdgcn_exp2f(fmaf(z[x][r + 1], a.scale_log2, -ref[x]));
-    l[x] += p0;
-    l[x] += p1;
-    pf[x][r >> 3][(r & 7) >> 1] = cvt_pk_bf16(p0, p1);
+  // Two scores to packed weights: pf[c] holds the keys 16 c + 8 (j / 4) +
+  // 4 hh + j % 4 of the step.
+  auto weigh = [&](int r, float ref, f32x16& z, u32x4 (&pf)[2]) {
+    const float p0 = __builtin_amdgcn_exp2f(fmaf(z[r], a.scale_log2, -ref));
+    const float p1 = __builtin_amdgcn_exp2f(fmaf(z[r + 1], a.scale_log2, -ref));
+    l += p0;
+    l += p1;
+    pf[r >> 3][(r & 7) >> 1] = cvt_pk_bf16(p0, p1);
   };
 
   // V^T: lane (dim, hh) of tile d wants the rows 16 c + 4 hh + 0..3 and those
@@ -832,7 +828,7 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, c
       const int piece = 4 * d + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
       voff[d][e] = k * ROWB + ((piece ^ swizzle<ROWB>(k)) << 4) + 8 * (lane & 1);
     }
-  auto values = [&](int i, const u32x4 (&pf)[2][2]) {
+  auto values = [&](int i, const u32x4 (&pf)[2]) {
     const uint32_t st = lds_address(vring + (i % NB) * STAGE);
 #pragma unroll
     for (int d = 0; d < D / 32; d += 2) {
@@ -843,10 +839,7 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, c
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            acc[x][d + e] = mfma32(vf[2 * e + k], pf[x][k], acc[x][d + e]);
+        for (int e = 0; e < 2; ++e) acc[d + e] = mfma32(vf[2 * e + k], pf[k], acc[d + e]);
     }
   };
 
@@ -856,7 +849,9 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, c
   };
 
   if (steps > 0) {
-    f32x16 z[2];
+    f32x16 z, nil;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) nil[r] = 0.f;
     Rows last;   // of the step that V is staged next
 #pragma unroll
     for (int i = 0; i < NB; ++i) {   // K of steps 0 .. NB - 1, V of 0 .. NB - 2
@@ -884,7 +879,7 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, c
     }
     wait_lds();
     meet();
-    zero(z);
+    z = nil;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) score(0, s, z);
     for (int i = 0; i < steps; ++i) {
@@ -906,84 +901,66 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, c
         stage(0, i + NB, last);
       }
       look(i, z);
-      const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-      f32x16 next[2];
-      u32x4 pf[2][2];
-      zero(next);
+      const float ref = m == -INFINITY ? 0.f : m;
+      f32x16 next = nil;
+      u32x4 pf[2];
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
         score(i + 1, s, next);
 #pragma unroll
-        for (int e = 0; e < 256 / D; ++e) {
-          const int w = s * (256 / D) + e;   // 16 pairs: 8 of each column tile
-          weigh(w >> 3, 2 * (w & 7), ref, z, pf);
-        }
+        for (int e = 0; e < 128 / D; ++e) weigh(2 * (s * (128 / D) + e), ref, z, pf);
       }
       values(i, pf);
-      z[0] = next[0];
-      z[1] = next[1];
+      z = next;
     }
   }
   wait_loads<0>();
   wait_lds();
-  const bool nan = __ballot(bad) != 0;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    if (nan) l[x] = NAN;
-    l[x] += __shfl_xor(l[x], 32);
-  }
+  if (__ballot(bad)) l = NAN;
+  l += __shfl_xor(l, 32);
 
   const bool whole = it.pieces == 1;
   const int item = (it.first + it.piece) * a.kv_heads + it.head;
   if (KG == 1) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int row = 64 * rg + 32 * x + n;
-      if (row >= t.rows) continue;
-      const int qi = (t.row0 + row) / a.group;
-      uint16_t* o = a.out + ((int64_t)(t.first_q + qi) * a.heads + it.head * a.group +
-                             (t.row0 + row) - qi * a.group) * D;
-      const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];   // a row that sees nothing: zeros
-      if (!whole && hh == 0) {
-        float* p = ml_at(a, c, D, item) + row * 2;
-        p[0] = m[x];
-        p[1] = l[x];
-      }
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const f32x4 v = {acc[x][d][4 * r], acc[x][d][4 * r + 1], acc[x][d][4 * r + 2],
-                           acc[x][d][4 * r + 3]};
-          const int d0 = 32 * d + 8 * r + 4 * hh;
-          if (whole)
-            *reinterpret_cast<u32x2*>(o + d0) =
-                u32x2{cvt_pk_bf16(v[0] * inv, v[1] * inv), cvt_pk_bf16(v[2] * inv, v[3] * inv)};
-          else
-            *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + (size_t)row * D + d0) = v;
-        }
+    const int row = 32 * rg + n;
+    if (row >= t.rows) return;
+    uint16_t* o = a.out + ((int64_t)(t.first_q + qi) * a.heads + it.head * a.group + my -
+                           qi * a.group) * D;
+    const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing: zeros
+    if (!whole && hh == 0) {
+      float* p = ml_at(a, c, D, item) + row * 2;
+      p[0] = m;
+      p[1] = l;
     }
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const f32x4 v = {acc[d][4 * r], acc[d][4 * r + 1], acc[d][4 * r + 2], acc[d][4 * r + 3]};
+        const int d0 = 32 * d + 8 * r + 4 * hh;
+        if (whole)
+          *reinterpret_cast<u32x2*>(o + d0) =
+              u32x2{cvt_pk_bf16(v[0] * inv, v[1] * inv), cvt_pk_bf16(v[2] * inv, v[3] * inv)};
+        else
+          *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + (size_t)row * D + d0) = v;
+      }
     return;
   }
   // Join of the groups: [group][row] m, l, then [group][row][D] sums.
   __syncthreads();
   float* ml = reinterpret_cast<float*>(smem);
   float* sums = ml + KG * R * 2;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int at = kg * R + 64 * rg + 32 * x + n;
-    if (hh == 0) {
-      ml[at * 2] = m[x];
-      ml[at * 2 + 1] = l[x];
-    }
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<f32x4*>(sums + at * D + 32 * d + 8 * r + 4 * hh) =
-            f32x4{acc[x][d][4 * r], acc[x][d][4 * r + 1], acc[x][d][4 * r + 2],
-                  acc[x][d][4 * r + 3]};
+  const int at = kg * R + 32 * rg + n;
+  if (hh == 0) {
+    ml[at * 2] = m;
+    ml[at * 2 + 1] = l;
   }
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<f32x4*>(sums + at * D + 32 * d + 8 * r + 4 * hh) =
+          f32x4{acc[d][4 * r], acc[d][4 * r + 1], acc[d][4 * r + 2], acc[d][4 * r + 3]};
   __syncthreads();
   constexpr int TPR = D / 4, RPP = 256 / TPR;   // threads a row, rows a pass
   for (int row = threadIdx.x / TPR; row < t.rows; row += RPP) {
@@ -1002,7 +979,7 @@ __global__ __launch_bounds__(256, 1) void attend_many_kernel(const AttnArgs a, c
     }
     if (whole) {
       v *= tot == 0.f ? 0.f : 1.f / tot;
-      const int qi = (t.row0 + row) / a.group;
+      const int qi = a.by_group.of(t.row0 + row);
       uint16_t* o = a.out + ((int64_t)(t.first_q + qi) * a.heads + it.head * a.group +
                              (t.row0 + row) - qi * a.group) * D;
       *reinterpret_cast<u32x2*>(o + d0) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
@@ -1024,52 +1001,85 @@ int64_t most_tiles(const AttnArgs& a, int R) {
   return all < by_seq ? all : by_seq;
 }
 
-// Rows a tile: 16 for tokens by themselves, otherwise 64 RG.  See run().
-int rows_per_tile(const AttnArgs& a) {
-  if ((int64_t)a.max_q * a.group <= 16) return 16;
-  return (int64_t)a.tokens * a.group / 256 * a.kv_heads >= 128 ? 256 : 64;
-}
+// How a call is carried out: sequences of up to 16 rows on the 16-row kernel,
+// others on tiles of 64 or 256.  Both kinds in one call are two launches, each
+// with a plan of its own sequences.
+struct Way {
+  Cut cut[2];        // few rows, many rows; R = 0: no such sequences
+  int items[2];      // grids
+  size_t bytes;      // workspace
+};
 
-Cut cut_of(const AttnArgs& a) {
-  const int R = rows_per_tile(a);
-  return R == 16 ? Cut{R, 1024, 4} : Cut{R, 256, 16};
-}
-
-// Items that the plan can have at most (and the grid).
+// Items that the plan can have at most.
 int64_t most_items(const AttnArgs& a, const Cut& c) {
-  return most_tiles(a, c.R) * a.kv_heads + c.target + 8;
+  return most_tiles(a, c.R) * a.kv_heads + (c.share != 0.f ? c.target + 8 : 0);
 }
 
-// Whether a tile can be cut at all: blocks_of() past min_blocks.
-bool may_cut(const AttnArgs& a, const Cut& c) {
-  return ((int64_t)a.width * a.page + 31) / 32 + 1 > c.min_blocks;
+Way way_of(const AttnArgs& a) {
+  Way w{};
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  const int kAll = 2147483647;
+  w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 256, 1024, 4, 16, 0, 16, 0.f};
+  if (rows > 16) {
+    const int64_t all = (int64_t)a.tokens * a.group;
+    const int R = all / 128 * a.kv_heads >= 200 && all / a.seqs >= 128 ? 128 : 64;
+    if (a.seqs == 1) w.cut[0].R = 0;   // one sequence: one launch, whatever its length
+    w.cut[1] = Cut{R, 512, 512, 8, 64, w.cut[0].R ? 16 : 0, kAll, 0.f};
+  }
+  for (int k = 0; k < 2; ++k) {
+    Cut& c = w.cut[k];
+    if (!c.R) continue;
+    // cut only where a tile can be longer than the shortest piece, and, for
+    // many rows, where the tiles by themselves do not fill the card
+    const bool may = ((int64_t)a.width * a.page + 31) / 32 + 1 > c.min_blocks &&
+                     (k == 0 || (int64_t)a.tokens * a.group / c.R * a.kv_heads < 2 * c.target);
+    c.share = may ? (float)a.kv_heads / (float)c.round : 0.f;
+    AttnArgs b = a;
+    if (k == 0 && rows > 16) b.max_q = 16 / a.group;
+    w.items[k] = (int)most_items(b, c);
+    if (may) {
+      const size_t n = (size_t)w.items[k] * c.R * (a.dim + 2) * sizeof(float);
+      if (n > w.bytes) w.bytes = n;
+    }
+  }
+  return w;
 }
 
 template <int D, bool Q8>
 hipError_t run(AttnArgs a, hipStream_t s) {
-  const Cut c = cut_of(a);
-  const bool cut = may_cut(a, c);
-  a.items = (int)(cut ? most_items(a, c) : most_tiles(a, c.R) * a.kv_heads);
-  if (c.R == 16)
-    attend_rows16_kernel<D, Q8, 4, 2><<<a.items, 256, 0, s>>>(a, c);
-  else if (c.R == 64)
-    attend_many_kernel<D, Q8, 1><<<a.items, 256, 0, s>>>(a, c);
-  else
-    attend_many_kernel<D, Q8, 4><<<a.items, 256, 0, s>>>(a, c);
-  if (cut) {
-    const int64_t joins = most_tiles(a, c.R) * a.kv_heads * ((c.R + 3) / 4);
-    join_pieces_kernel<D><<<(unsigned)joins, 256, 0, s>>>(a, c);
+  a.by_group = divisor(a.group);
+  a.by_page = divisor(a.page);
+  a.by_heads = divisor(a.kv_heads);
+  const Way w = way_of(a);
+  // the launches follow each other on the stream and share the workspace
+  for (int k = 1; k >= 0; --k) {
+    const Cut& c = w.cut[k];
+    if (!c.R) continue;
+    a.items = w.items[k];
+    if (c.R == 16)
+      attend_rows16_kernel<D, Q8, 4, 2><<<a.items, 256, 0, s>>>(a, c);
+    else if (c.R == 64)
+      attend_many_kernel<D, Q8, 2><<<a.items, 256, 0, s>>>(a, c);
+    else
+      attend_many_kernel<D, Q8, 4><<<a.items, 256, 0, s>>>(a, c);
+    if (c.share != 0.f) {
+      const int64_t joins = (a.items - c.target - 8) * (int64_t)(c.R == 16 ? 4 : c.R / 16);
+      join_pieces_kernel<D><<<(unsigned)joins, 256, 0, s>>>(a, c);
+    }
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t paged_attention_workspace(const AttnArgs& a) {
-  const Cut c = cut_of(a);
-  if (!may_cut(a, c)) return 0;
-  return (size_t)most_items(a, c) * c.R * (a.dim + 2) * sizeof(float);
+Divisor divisor(int by) {
+  Divisor d{1, 0, by};
+  while ((int64_t(1) << d.shift) < by) ++d.shift;
+  d.mul = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << d.shift) - by)) / by + 1);
+  return d;
 }
+
+size_t paged_attention_workspace(const AttnArgs& a) { return way_of(a).bytes; }
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t s) {
   const bool q8 = a.scale[0] != nullptr;

@@ -38,6 +38,16 @@ struct KvArgs {
 hipError_t launch_kv_write(const KvArgs& a, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& a, hipStream_t stream);
 
+// Division of 0 <= x < 2^31 by a number that the host knows.
+struct Divisor {
+  uint32_t mul, shift;
+  int by;
+  __device__ __forceinline__ int of(int x) const {
+    return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift);
+  }
+};
+Divisor divisor(int by);
+
 struct AttnArgs {
   const uint16_t* q;         // [tokens, heads, dim] with strides
   const uint8_t* cache[2];   // k, v: [pages, kv_heads, page, dim]
@@ -50,6 +60,7 @@ struct AttnArgs {
   int64_t q_token_stride, q_head_stride;
   int64_t pages;
   int tokens, seqs, max_q, heads, kv_heads, group, dim, page, width;
+  Divisor by_group, by_page, by_heads;   // group, page, kv_heads (set by the launcher)
   int window;                // 0: none
   int items;                 // pieces that the workspace has room for (set by the launcher)
   float scale_log2;          // softmax scale * log2(e)
