@@ -496,7 +496,8 @@ int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_
  *   workspace device, >= bitdelta_paged_attention_workspace_size(...) bytes
  *             (0 bytes: may be NULL); contents are scratch
  * heads is a multiple of kv_heads, at most 1024 and 64 times kv_heads; tokens
- * times heads below 2^30, width * page and max_q below 2^31, seqs at most 65535.
+ * times heads below 2^30, width * page at most 2^30, max_q below 2^31, seqs at
+ * most 65535.
  */
 size_t bitdelta_paged_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t max_q,
                                                int64_t heads, int64_t kv_heads, int64_t dim,

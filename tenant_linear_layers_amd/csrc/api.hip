@@ -540,7 +540,7 @@ bool attention_shape_ok(int64_t tokens, int64_t seqs, int64_t max_q, int64_t hea
   return cache_shape_ok(kv_heads, dim, 1, page) && heads >= kv_heads && heads <= 1024 &&
          heads % kv_heads == 0 && heads / kv_heads <= 64 && tokens >= 0 &&
          tokens <= (kInt32Max >> 1) / heads && seqs >= 0 && seqs <= 65535 && max_q >= 0 &&
-         max_q <= kInt32Max && width >= 0 && width <= kInt32Max / page;
+         max_q <= kInt32Max && width >= 0 && width <= (int64_t(1) << 30) / page;
 }
 
 bd::AttnArgs attention_sizes(int64_t tokens, int64_t seqs, int64_t max_q, int64_t heads,
@@ -617,7 +617,9 @@ BD_EXPORT int bitdelta_paged_attention(
   a.cu_q = cu_q;
   a.kv_len = kv_len;
   a.pages = pages;
-  a.window = (int)(window < kInt32Max ? window : kInt32Max);
+  // a window that no sequence can fill hides nothing; what is left keeps
+  // positions minus the window inside an int
+  a.window = (int)(window < width * page ? window : 0);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = out;
   a.partial = static_cast<float*>(workspace);

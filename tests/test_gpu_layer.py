@@ -448,3 +448,11 @@ def test_paged_attention_refusals():
             bad()
     none = T.paged_attention(q[:0], c[0], c[1], t[:0], cu[:1], kv[:0], 0)
     assert none.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 40, 64, 31, 32])
+def test_paged_attention_windows_wider_than_any_sequence(window):
+    """A window hides nothing from a sequence that does not fill it, also where
+    the sequence's first rows stand before key 0 and see none."""
+    p = _problem([4, 40, 1], [2, 25, 31], 8, 2, 64, 16, False, seed=15)
+    _check(p, _call(p, window=window), window=min(window, 10 ** 6))

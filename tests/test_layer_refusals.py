@@ -91,6 +91,16 @@ def test_paged_attention_argument_errors():
     assert T.paged_attention_workspace_size(5, 2, 4, 9, 2, 128, 3, 16) == 0
 
 
+def test_paged_attention_refuses_sequences_past_2_to_30_keys():
+    """Positions, less a window, have to fit 32 bits."""
+    size = T.paged_attention_workspace_size
+    assert size(1, 1, 1, 8, 8, 128, 1 << 26, 16) > 0
+    assert size(1, 1, 1, 8, 8, 128, (1 << 26) + 1, 16) == 0
+    f = T.lib().bitdelta_paged_attention
+    assert f(A, 1024, 128, B, C, None, None, D, D + 4096, D + 8192, 1, 1, 1, 8, 8, 128, 4, 16,
+             (1 << 26) + 1, 1.0, 0, E, F, 1 << 40, None) == 2
+
+
 # ------------------------------------------------------------------ binding
 def test_binding_refuses_host_tensors_and_non_tensors():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
