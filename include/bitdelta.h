@@ -492,6 +492,7 @@ int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_
  *   cu_q      device, int32 [seqs + 1], rising; held to [0, tokens].  Rows of
  *             out that no sequence has are not written.
  *   max_q     the largest n; rows past it may not be computed
+ *   scale     above 0 and finite, as is its product with log2(e)
  *   out       device, bf16 [tokens, heads, dim], contiguous, written
  *   workspace device, >= bitdelta_paged_attention_workspace_size(...) bytes
  *             (0 bytes: may be NULL); contents are scratch

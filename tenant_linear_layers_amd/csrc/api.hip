@@ -2,6 +2,7 @@
 // Every check runs on the host before anything is enqueued; see
 // include/bitdelta.h for the contract of each entry point.
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -576,8 +577,12 @@ BD_EXPORT int bitdelta_paged_attention(
     int64_t heads, int64_t kv_heads, int64_t dim, int64_t pages, int64_t page, int64_t width,
     float scale, int64_t window, uint16_t* out, void* workspace, size_t workspace_bytes,
     void* stream) {
+  // the running maximum is taken of the unscaled scores: scale must keep their
+  // order, and -infinity times it must stay -infinity
+  const float scale_log2 = scale * 1.4426950408889634f;
   if (!attention_shape_ok(tokens, seqs, max_q, heads, kv_heads, dim, width, page) ||
-      !cache_shape_ok(kv_heads, dim, pages, page) || window < 0 || q_token_stride < 0 ||
+      !cache_shape_ok(kv_heads, dim, pages, page) || window < 0 ||
+      !(scale_log2 >= 1.17549435e-38f && scale_log2 < INFINITY) || q_token_stride < 0 ||
       q_head_stride < 0 || q_token_stride >= kMaxElems || q_head_stride >= kMaxElems)
     return BITDELTA_ERR_SHAPE;
   if (tokens == 0 || seqs == 0 || max_q == 0) return BITDELTA_OK;
@@ -620,7 +625,7 @@ BD_EXPORT int bitdelta_paged_attention(
   // a window that no sequence can fill hides nothing; what is left keeps
   // positions minus the window inside an int
   a.window = (int)(window < width * page ? window : 0);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.out = out;
   a.partial = static_cast<float*>(workspace);
   return status_of(bd::launch_paged_attention(a, static_cast<hipStream_t>(stream)));

@@ -230,7 +230,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     [seqs, width] page ids; cu_q: int32 [seqs + 1], the sequences' rows of q;
     kv_len: int32 [seqs], cached keys of each, the new tokens' among them;
     max_q: the most rows of a sequence; window: keys a row sees, 0 for all;
-    scale: of the scores, 1 / sqrt(dim) by default.  A row that sees no key
+    scale: of the scores, above 0, 1 / sqrt(dim) by default.  A row that sees no key
     gives zeros."""
     dev = _device(q, "q")
     pages, kv_heads, page, dim, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)

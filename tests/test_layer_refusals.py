@@ -101,6 +101,13 @@ def test_paged_attention_refuses_sequences_past_2_to_30_keys():
              (1 << 26) + 1, 1.0, 0, E, F, 1 << 40, None) == 2
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.125, -0.0, 1e-40, math.inf, -math.inf, math.nan, 3e38])
+def test_paged_attention_refuses_scales_that_do_not_keep_the_scores_order(scale):
+    f = T.lib().bitdelta_paged_attention
+    assert f(A, 1024, 128, B, C, None, None, D, D + 4096, D + 8192, 1, 1, 1, 8, 8, 128, 4, 16, 1,
+             scale, 0, E, F, 1 << 40, None) == 2
+
+
 # ------------------------------------------------------------------ binding
 def test_binding_refuses_host_tensors_and_non_tensors():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
