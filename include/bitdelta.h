@@ -427,8 +427,8 @@ int bitdelta_monosoup_merge(const uint16_t* const* w_ft, int32_t k, const uint16
  * becomes e4m3's NaN and has no part in the scale.
  *
  * bitdelta_rms_norm - h = x + residual; y = h / sqrt(mean(h^2) + eps) * w.
- * Sums are float32, taken of the unrounded h.  Without a residual (NULL, with
- * h_out NULL) h is x.
+ * Sums are float32, taken of the unrounded h (a row whose sum of squares
+ * passes 2^128 gives zeros).  Without a residual (NULL, with h_out NULL) h is x.
  *   x, residual   device, bf16 [rows, cols], rows x_stride / r_stride
  *                 elements apart
  *   w             device, bf16 [cols]
@@ -455,8 +455,9 @@ int bitdelta_rms_norm_mx(const uint16_t* x, int64_t x_stride, const uint16_t* re
  * and, times heads, at most 2^35.
  *
  * bitdelta_kv_write puts row t of k and v into slot slots[t]; a slot outside
- * the cache (a negative one for padding) is passed over, and of tokens with
- * one slot any may stay.  k, v: device, bf16 [tokens, heads, dim], tokens and
+ * the cache (a negative one for padding) is passed over.  The slots of a call
+ * have to differ: where two tokens name one, its row may be a mixture of theirs.
+ * k, v: device, bf16 [tokens, heads, dim], tokens and
  * heads the given strides (in elements) apart, the dims contiguous.
  *
  * bitdelta_kv_read writes the rows at slots[t] to k and v, bf16
@@ -482,7 +483,8 @@ int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_
  * j > p - window:
  *   out[i] = sum_j softmax_j(scale * q[i] . k[j]) v[j]
  * Query head h reads key/value head h / (heads / kv_heads).  A row that sees
- * no key is zero.  Scores, maxima and sums are float32; the probabilities
+ * no key is zero.  NaN and infinities in the cache or in q reach the rows that
+ * see them only.  Scores, maxima and sums are float32; the probabilities
  * are rounded to bf16 for the product with v.
  *   q         device, bf16 [tokens, heads, dim], strides in elements
  *   table     device, int32 [seqs, width]; entries of pages that no row sees

@@ -42,6 +42,7 @@ struct Tile {
   int pos0;           // position of query 0 of the sequence
   int lo, hi;         // keys that some row of the tile sees
   int all_lo, all_hi; // keys that every row of the tile sees
+  int i0, i1;         // its first and last query
 };
 
 __device__ __forceinline__ void seq_range(const AttnArgs& a, int b, int& q0, int& n, int& len) {
@@ -56,11 +57,12 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, int q0, int n, int le
   x.row0 = t * R;
   x.rows = min(R, n * a.group - x.row0);
   x.pos0 = len - n;
-  const int i0 = a.by_group.of(x.row0), i1 = a.by_group.of(x.row0 + x.rows - 1);
-  x.hi = max(min(len, x.pos0 + i1 + 1), 0);
-  x.lo = a.window ? max(x.pos0 + i0 - a.window + 1, 0) : 0;
-  x.all_hi = x.pos0 + i0 + 1;
-  x.all_lo = a.window ? x.pos0 + i1 - a.window + 1 : 0;
+  x.i0 = a.by_group.of(x.row0);
+  x.i1 = a.by_group.of(x.row0 + x.rows - 1);
+  x.hi = max(min(len, x.pos0 + x.i1 + 1), 0);
+  x.lo = a.window ? max(x.pos0 + x.i0 - a.window + 1, 0) : 0;
+  x.all_hi = x.pos0 + x.i0 + 1;
+  x.all_lo = a.window ? x.pos0 + x.i1 - a.window + 1 : 0;
   if (x.lo >= x.hi) x.lo = x.hi = 0;
   return x;
 }
@@ -257,6 +259,45 @@ __global__ __launch_bounds__(256) void join_pieces_kernel(const AttnArgs a, cons
   }
 }
 
+// ------------------------------------------------------------------ NaN, infinities
+// A weight of zero times NaN or infinity is NaN, and the product with V takes
+// every key of a step for every row of a tile: a value that is not finite
+// would reach rows that do not see it, such as those of the tokens before its
+// own.  So a tile whose rows do not all see the same keys looks at its sums
+// once they are complete.  Where a row's sums are not finite though its total
+// weight is, the item is gone through again for one query at a time, whose
+// rows see the same keys; keys outside are read as zeros.
+__device__ __forceinline__ bool workgroup_any(bool mine, void* lds) {
+  int* found = static_cast<int*>(lds);
+  __syncthreads();
+  if (threadIdx.x == 0) *found = 0;
+  __syncthreads();
+  if (mine) *found = 1;
+  __syncthreads();
+  const int any = *found;
+  __syncthreads();
+  return any != 0;
+}
+
+// Is one of N sums not finite?
+template <int N, typename V>
+__device__ __forceinline__ bool not_finite(const V* v) {
+  float zero = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int r = 0; r < (int)(sizeof(V) / 4); ++r) zero = fmaf(v[i][r], 0.f, zero);
+  return zero != 0.f;
+}
+
+// The keys of [lo, hi) that query i sees.
+__device__ __forceinline__ void query_range(const AttnArgs& a, const Tile& t, int i, int& lo,
+                                            int& hi) {
+  hi = min(hi, t.pos0 + i + 1);
+  if (a.window) lo = max(lo, t.pos0 + i - a.window + 1);
+  if (lo >= hi) lo = hi = 0;
+}
+
 // ------------------------------------------------------------------ reads of V
 // Transposing LDS reads: 16 lanes read 8 bytes each, together a block of four
 // rows of 16 bf16 (eight rows of 16 bytes), and lane n of them gets column n.
@@ -351,12 +392,7 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g4 = lane >> 4;
   const Tile t = tile_of(a, it.q0, it.n, it.len, it.tile, R);
-  int lo, hi;
-  piece_range(t, it.piece, it.pieces, lo, hi);
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
-  const int kbeg = (lo & ~31) + 32 * wv;
-  const int steps = hi > kbeg ? (hi - kbeg + 32 * NW - 1) / (32 * NW) : 0;
+  int lo, hi, kbeg, steps, vis_hi;   // of a pass
 
   // Q^T: lane n's row, the dims that the lane's K pieces hold.
   u32x4 qf[D / 32];
@@ -371,7 +407,7 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
     qf[s] = *reinterpret_cast<const u32x4_any*>(qp + d0);
   }
   const int pos = t.pos0 + qi;
-  const int vis_hi = min(pos + 1, hi), vis_lo = a.window ? pos - a.window + 1 : 0;
+  const int vis_lo = a.window ? pos - a.window + 1 : 0;
 
   char* ring = smem + wv * U * 2 * STAGE;
   int voff[IPH];
@@ -433,9 +469,7 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
   };
 
   f32x4 acc[D / 16];
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;
+  float m, l;
 
   auto step = [&](int i, int u) {
     const int key0 = kbeg + 32 * NW * i;
@@ -536,80 +570,104 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
     }
   };
 
-  if (steps > 0) {
+  int only = -1;   // the query of this pass, or all
+  for (;;) {
+    piece_range(t, it.piece, it.pieces, lo, hi);
+    if (only >= 0) query_range(a, t, only, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    kbeg = (lo & ~31) + 32 * wv;
+    steps = hi > kbeg ? (hi - kbeg + 32 * NW - 1) / (32 * NW) : 0;
+    vis_hi = min(pos + 1, hi);
 #pragma unroll
-    for (int u = 0; u < U - 1; ++u) issue(u, u, u == 0);
-    for (int i0 = 0; i0 < steps; i0 += U) {
+    for (int d = 0; d < D / 16; ++d) acc[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    m = -INFINITY;
+    l = 0.f;
+    if (steps > 0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u;
-        // the stage to be filled was read by the step before: those reads are
-        // complete before loads may write it (a load to LDS is not ordered
-        // after earlier reads of its wave)
-        wait_lds();
-        // past the last step the loads have no rows left and read nothing:
-        // every step issues the same number
-        issue(i + U - 1, (u + U - 1) % U, false);
-        if (i < steps) {
-          wait_loads<HALF * 2 * (U - 1) + HALF>();
-          step(i, u);
+      for (int u = 0; u < U - 1; ++u) issue(u, u, u == 0);
+      for (int i0 = 0; i0 < steps; i0 += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u;
+          // the stage to be filled was read by the step before: those reads are
+          // complete before loads may write it (a load to LDS is not ordered
+          // after earlier reads of its wave)
+          wait_lds();
+          // past the last step the loads have no rows left and read nothing:
+          // every step issues the same number
+          issue(i + U - 1, (u + U - 1) % U, false);
+          if (i < steps) {
+            wait_loads<HALF * 2 * (U - 1) + HALF>();
+            step(i, u);
+          }
         }
       }
     }
-  }
-  wait_loads<0>();
-  if (__ballot(bad)) l = NAN;
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+    wait_loads<0>();
+    if (__ballot(bad)) l = NAN;
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (only < 0 && (t.all_hi < hi || t.all_lo > lo) &&
+        workgroup_any(fabsf(l) < INFINITY && not_finite<D / 16>(acc), smem)) {
+      only = t.i0;
+      continue;
+    }
 
-  // Join of the waves: [wave][row] m, l, then [wave][row][D] sums.
-  __syncthreads();
-  float* ml = reinterpret_cast<float*>(smem);
-  float* sums = ml + NW * R * 2;
-  if (g4 == 0) {
-    ml[(wv * R + n) * 2] = m;
-    ml[(wv * R + n) * 2 + 1] = l;
-  }
+    // Join of the waves: [wave][row] m, l, then [wave][row][D] sums.
+    __syncthreads();
+    float* ml = reinterpret_cast<float*>(smem);
+    float* sums = ml + NW * R * 2;
+    if (g4 == 0) {
+      ml[(wv * R + n) * 2] = m;
+      ml[(wv * R + n) * 2 + 1] = l;
+    }
 #pragma unroll
-  for (int dt = 0; dt < D / 16; ++dt)
-    *reinterpret_cast<f32x4*>(sums + (wv * R + n) * D + dt * 16 + 4 * g4) = acc[dt];
-  __syncthreads();
-  constexpr int TPR = NW * 64 / R;          // threads a row
-  const int row = threadIdx.x / TPR;
-  if (row >= t.rows) return;
-  float top = -INFINITY;
+    for (int dt = 0; dt < D / 16; ++dt)
+      *reinterpret_cast<f32x4*>(sums + (wv * R + n) * D + dt * 16 + 4 * g4) = acc[dt];
+    __syncthreads();
+    constexpr int TPR = NW * 64 / R;          // threads a row
+    const int row = threadIdx.x / TPR;
+    const int i = a.by_group.of(t.row0 + row);
+    if (row < t.rows && (only < 0 || i == only)) {
+      float top = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[(w * R + row) * 2]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float f[NW], tot = 0.f;
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[(w * R + row) * 2]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float f[NW], tot = 0.f;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    f[w] = __builtin_amdgcn_exp2f(ml[(w * R + row) * 2] - ref);
-    tot += f[w] * ml[(w * R + row) * 2 + 1];
-  }
-  const bool whole = it.pieces == 1;
-  const float inv = !whole ? 1.f : tot == 0.f ? 0.f : 1.f / tot;  // a row that sees nothing: zeros
-  const int i = a.by_group.of(t.row0 + row);
-  uint16_t* o = a.out + ((int64_t)(t.first_q + i) * a.heads + it.head * a.group + (t.row0 + row) -
-                         i * a.group) * D;
-  const int item = (it.first + it.piece) * a.kv_heads + it.head;
-  if (!whole && threadIdx.x % TPR == 0) {
-    float* p = ml_at(a, c, D, item) + row * 2;
-    p[0] = top;
-    p[1] = tot;
-  }
+      for (int w = 0; w < NW; ++w) {
+        f[w] = __builtin_amdgcn_exp2f(ml[(w * R + row) * 2] - ref);
+        tot += f[w] * ml[(w * R + row) * 2 + 1];
+      }
+      const bool whole = it.pieces == 1;
+      // a row that sees nothing: zeros
+      const float inv = !whole ? 1.f : tot == 0.f ? 0.f : 1.f / tot;
+      uint16_t* o = a.out + ((int64_t)(t.first_q + i) * a.heads + it.head * a.group +
+                             (t.row0 + row) - i * a.group) * D;
+      const int item = (it.first + it.piece) * a.kv_heads + it.head;
+      if (!whole && threadIdx.x % TPR == 0) {
+        float* p = ml_at(a, c, D, item) + row * 2;
+        p[0] = top;
+        p[1] = tot;
+      }
 #pragma unroll
-  for (int k = 0; k < D / (4 * TPR); ++k) {
-    const int d0 = (k * TPR + threadIdx.x % TPR) * 4;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < D / (4 * TPR); ++k) {
+        const int d0 = (k * TPR + threadIdx.x % TPR) * 4;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
-      v += f[w] * *reinterpret_cast<const f32x4*>(sums + (w * R + row) * D + d0);
-    v *= inv;
-    if (whole)
-      *reinterpret_cast<u32x2*>(o + d0) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
-    else
-      *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + row * D + d0) = v;
+        for (int w = 0; w < NW; ++w)
+          v += f[w] * *reinterpret_cast<const f32x4*>(sums + (w * R + row) * D + d0);
+        v *= inv;
+        if (whole)
+          *reinterpret_cast<u32x2*>(o + d0) =
+              u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+        else
+          *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + row * D + d0) = v;
+      }
+    }
+    if (only < 0 || ++only > t.i1) return;
+    __syncthreads();
   }
 }
 
@@ -654,13 +712,7 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
   const int rg = wv % RG, kg = wv / RG;
   const int n = lane & 31, hh = lane >> 5;
   const Tile t = tile_of(a, it.q0, it.n, it.len, it.tile, R);
-  int lo, hi;
-  piece_range(t, it.piece, it.pieces, lo, hi);
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
-  const int kbeg = (lo & ~31) + 32 * kg;
-  const int steps = __builtin_amdgcn_readfirstlane(
-      hi > lo ? (hi - (lo & ~31) + 32 * KG - 1) / (32 * KG) : 0);   // of every group
+  int lo, hi, kbeg, steps, vis_hi, all_hi;   // of a pass
 
   // Q^T of the wave's rows and what each of them sees
   u32x4 qf[D / 16];
@@ -671,12 +723,10 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
 #pragma unroll
   for (int s = 0; s < D / 16; ++s)
     qf[s] = *reinterpret_cast<const u32x4_any*>(qp + 16 * s + 8 * hh);
-  const int vis_hi = min(t.pos0 + qi + 1, hi);
   const int vis_lo = a.window ? t.pos0 + qi - a.window + 1 : 0;
   // the first and last query of the wave's rows: keys that all of them see
   const int first_q = a.by_group.of(t.row0 + min(32 * rg, t.rows - 1));
   const int last_q = a.by_group.of(t.row0 + min(32 * rg + 31, t.rows - 1));
-  const int all_hi = __builtin_amdgcn_readfirstlane(min(t.pos0 + first_q + 1, hi));
   const int all_lo =
       __builtin_amdgcn_readfirstlane(a.window ? t.pos0 + last_q - a.window + 1 : 0);
 
@@ -768,11 +818,7 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
   };
 
   f32x16 acc[D / 32];
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[d][r] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  float m, l;
 
   // one sixteen of the dims of the scores of step i
   auto score = [&](int i, int s, f32x16& z) {
@@ -848,149 +894,178 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  if (steps > 0) {
-    f32x16 z, nil;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) nil[r] = 0.f;
-    Rows last;   // of the step that V is staged next
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {   // K of steps 0 .. NB - 1, V of 0 .. NB - 2
-      last = rows_of(i);
-      if (Q8) {
-        fetch(0, last);
-        put(0, i);
-      } else {
-        stage(0, i, last);
-      }
-      if (i == NB - 1) break;
-      if (Q8) {
-        fetch(1, last);
-        put(1, i);
-      } else {
-        stage(1, i, last);
-      }
-    }
-    if (Q8) {
-      fetch(1, last);
-      last = rows_of(NB);
-      fetch(0, last);
-    } else {
-      wait_loads<0>();
-    }
-    wait_lds();
-    meet();
-    z = nil;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) score(0, s, z);
-    for (int i = 0; i < steps; ++i) {
-      // K of step i + 1 and V of step i have arrived, and all waves have the
-      // scores of step i and the values of step i - 1 behind them: K's stage
-      // i and V's stage i - 1 may be written.
-      if (!Q8) wait_loads<(NB - 2) * 2 * MINE>();
-      wait_lds();
-      meet();
-      if (Q8) {
-        put(0, i + NB);
-        put(1, i + NB - 1);
-        fetch(1, last);
-        last = rows_of(i + NB + 1);
-        fetch(0, last);
-      } else {
-        stage(1, i + NB - 1, last);
-        last = rows_of(i + NB);
-        stage(0, i + NB, last);
-      }
-      look(i, z);
-      const float ref = m == -INFINITY ? 0.f : m;
-      f32x16 next = nil;
-      u32x4 pf[2];
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        score(i + 1, s, next);
-#pragma unroll
-        for (int e = 0; e < 128 / D; ++e) weigh(2 * (s * (128 / D) + e), ref, z, pf);
-      }
-      values(i, pf);
-      z = next;
-    }
-  }
-  wait_loads<0>();
-  wait_lds();
-  if (__ballot(bad)) l = NAN;
-  l += __shfl_xor(l, 32);
-
-  const bool whole = it.pieces == 1;
-  const int item = (it.first + it.piece) * a.kv_heads + it.head;
-  if (KG == 1) {
-    const int row = 32 * rg + n;
-    if (row >= t.rows) return;
-    uint16_t* o = a.out + ((int64_t)(t.first_q + qi) * a.heads + it.head * a.group + my -
-                           qi * a.group) * D;
-    const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing: zeros
-    if (!whole && hh == 0) {
-      float* p = ml_at(a, c, D, item) + row * 2;
-      p[0] = m;
-      p[1] = l;
-    }
+  int only = -1;   // the query of this pass, or all
+  for (;;) {
+    piece_range(t, it.piece, it.pieces, lo, hi);
+    if (only >= 0) query_range(a, t, only, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    kbeg = (lo & ~31) + 32 * kg;
+    steps = __builtin_amdgcn_readfirstlane(
+        hi > lo ? (hi - (lo & ~31) + 32 * KG - 1) / (32 * KG) : 0);   // of every group
+    vis_hi = min(t.pos0 + qi + 1, hi);
+    all_hi = __builtin_amdgcn_readfirstlane(min(t.pos0 + first_q + 1, hi));
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const f32x4 v = {acc[d][4 * r], acc[d][4 * r + 1], acc[d][4 * r + 2], acc[d][4 * r + 3]};
-        const int d0 = 32 * d + 8 * r + 4 * hh;
-        if (whole)
-          *reinterpret_cast<u32x2*>(o + d0) =
-              u32x2{cvt_pk_bf16(v[0] * inv, v[1] * inv), cvt_pk_bf16(v[2] * inv, v[3] * inv)};
-        else
-          *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + (size_t)row * D + d0) = v;
+      for (int r = 0; r < 16; ++r) acc[d][r] = 0.f;
+    m = -INFINITY;
+    l = 0.f;
+    if (steps > 0) {
+      f32x16 z, nil;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) nil[r] = 0.f;
+      Rows last;   // of the step that V is staged next
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {   // K of steps 0 .. NB - 1, V of 0 .. NB - 2
+        last = rows_of(i);
+        if (Q8) {
+          fetch(0, last);
+          put(0, i);
+        } else {
+          stage(0, i, last);
+        }
+        if (i == NB - 1) break;
+        if (Q8) {
+          fetch(1, last);
+          put(1, i);
+        } else {
+          stage(1, i, last);
+        }
       }
-    return;
-  }
-  // Join of the groups: [group][row] m, l, then [group][row][D] sums.
-  __syncthreads();
-  float* ml = reinterpret_cast<float*>(smem);
-  float* sums = ml + KG * R * 2;
-  const int at = kg * R + 32 * rg + n;
-  if (hh == 0) {
-    ml[at * 2] = m;
-    ml[at * 2 + 1] = l;
-  }
+      if (Q8) {
+        fetch(1, last);
+        last = rows_of(NB);
+        fetch(0, last);
+      } else {
+        wait_loads<0>();
+      }
+      wait_lds();
+      meet();
+      z = nil;
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d)
+      for (int s = 0; s < D / 16; ++s) score(0, s, z);
+      for (int i = 0; i < steps; ++i) {
+        // K of step i + 1 and V of step i have arrived, and all waves have the
+        // scores of step i and the values of step i - 1 behind them: K's stage
+        // i and V's stage i - 1 may be written.
+        if (!Q8) wait_loads<(NB - 2) * 2 * MINE>();
+        wait_lds();
+        meet();
+        if (Q8) {
+          put(0, i + NB);
+          put(1, i + NB - 1);
+          fetch(1, last);
+          last = rows_of(i + NB + 1);
+          fetch(0, last);
+        } else {
+          stage(1, i + NB - 1, last);
+          last = rows_of(i + NB);
+          stage(0, i + NB, last);
+        }
+        look(i, z);
+        const float ref = m == -INFINITY ? 0.f : m;
+        f32x16 next = nil;
+        u32x4 pf[2];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      *reinterpret_cast<f32x4*>(sums + at * D + 32 * d + 8 * r + 4 * hh) =
-          f32x4{acc[d][4 * r], acc[d][4 * r + 1], acc[d][4 * r + 2], acc[d][4 * r + 3]};
-  __syncthreads();
-  constexpr int TPR = D / 4, RPP = 256 / TPR;   // threads a row, rows a pass
-  for (int row = threadIdx.x / TPR; row < t.rows; row += RPP) {
-    float top = -INFINITY;
+        for (int s = 0; s < D / 16; ++s) {
+          score(i + 1, s, next);
 #pragma unroll
-    for (int w = 0; w < KG; ++w) top = fmaxf(top, ml[(w * R + row) * 2]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const int d0 = (threadIdx.x % TPR) * 4;
-    float tot = 0.f;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < KG; ++w) {
-      const float f = __builtin_amdgcn_exp2f(ml[(w * R + row) * 2] - ref);
-      tot += f * ml[(w * R + row) * 2 + 1];
-      v += f * *reinterpret_cast<const f32x4*>(sums + (w * R + row) * D + d0);
+          for (int e = 0; e < 128 / D; ++e) weigh(2 * (s * (128 / D) + e), ref, z, pf);
+        }
+        values(i, pf);
+        z = next;
+      }
     }
-    if (whole) {
-      v *= tot == 0.f ? 0.f : 1.f / tot;
-      const int qi = a.by_group.of(t.row0 + row);
-      uint16_t* o = a.out + ((int64_t)(t.first_q + qi) * a.heads + it.head * a.group +
-                             (t.row0 + row) - qi * a.group) * D;
-      *reinterpret_cast<u32x2*>(o + d0) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+    wait_loads<0>();
+    wait_lds();
+    if (__ballot(bad)) l = NAN;
+    l += __shfl_xor(l, 32);
+    if (only < 0 && (t.all_hi < hi || t.all_lo > lo) &&
+        workgroup_any(fabsf(l) < INFINITY && not_finite<D / 32>(acc), smem)) {
+      only = t.i0;
+      continue;
+    }
+
+    const bool whole = it.pieces == 1;
+    const int item = (it.first + it.piece) * a.kv_heads + it.head;
+    if (KG == 1) {
+      const int row = 32 * rg + n;
+      if (row < t.rows && (only < 0 || qi == only)) {
+        uint16_t* o = a.out + ((int64_t)(t.first_q + qi) * a.heads + it.head * a.group + my -
+                               qi * a.group) * D;
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees nothing: zeros
+        if (!whole && hh == 0) {
+          float* p = ml_at(a, c, D, item) + row * 2;
+          p[0] = m;
+          p[1] = l;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const f32x4 v = {acc[d][4 * r], acc[d][4 * r + 1], acc[d][4 * r + 2],
+                             acc[d][4 * r + 3]};
+            const int d0 = 32 * d + 8 * r + 4 * hh;
+            if (whole)
+              *reinterpret_cast<u32x2*>(o + d0) =
+                  u32x2{cvt_pk_bf16(v[0] * inv, v[1] * inv), cvt_pk_bf16(v[2] * inv, v[3] * inv)};
+            else
+              *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + (size_t)row * D + d0) = v;
+          }
+      }
     } else {
-      *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + (size_t)row * D + d0) = v;
-      if (d0 == 0) {
-        float* p = ml_at(a, c, D, item) + row * 2;
-        p[0] = top;
-        p[1] = tot;
+      // Join of the groups: [group][row] m, l, then [group][row][D] sums.
+      __syncthreads();
+      float* ml = reinterpret_cast<float*>(smem);
+      float* sums = ml + KG * R * 2;
+      const int at = kg * R + 32 * rg + n;
+      if (hh == 0) {
+        ml[at * 2] = m;
+        ml[at * 2 + 1] = l;
+      }
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<f32x4*>(sums + at * D + 32 * d + 8 * r + 4 * hh) =
+              f32x4{acc[d][4 * r], acc[d][4 * r + 1], acc[d][4 * r + 2], acc[d][4 * r + 3]};
+      __syncthreads();
+      constexpr int TPR = D / 4, RPP = 256 / TPR;   // threads a row, rows a pass
+      for (int row = threadIdx.x / TPR; row < t.rows; row += RPP) {
+        const int i = a.by_group.of(t.row0 + row);
+        if (only >= 0 && i != only) continue;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < KG; ++w) top = fmaxf(top, ml[(w * R + row) * 2]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const int d0 = (threadIdx.x % TPR) * 4;
+        float tot = 0.f;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < KG; ++w) {
+          const float f = __builtin_amdgcn_exp2f(ml[(w * R + row) * 2] - ref);
+          tot += f * ml[(w * R + row) * 2 + 1];
+          v += f * *reinterpret_cast<const f32x4*>(sums + (w * R + row) * D + d0);
+        }
+        if (whole) {
+          v *= tot == 0.f ? 0.f : 1.f / tot;
+          uint16_t* o = a.out + ((int64_t)(t.first_q + i) * a.heads + it.head * a.group +
+                                 (t.row0 + row) - i * a.group) * D;
+          *reinterpret_cast<u32x2*>(o + d0) =
+              u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+        } else {
+          *reinterpret_cast<f32x4*>(sums_at(a, c, D, item) + (size_t)row * D + d0) = v;
+          if (d0 == 0) {
+            float* p = ml_at(a, c, D, item) + row * 2;
+            p[0] = top;
+            p[1] = tot;
+          }
+        }
       }
     }
+    if (only < 0 || ++only > t.i1) return;
+    __syncthreads();
   }
 }
 

@@ -456,3 +456,55 @@ def test_paged_attention_windows_wider_than_any_sequence(window):
     the sequence's first rows stand before key 0 and see none."""
     p = _problem([4, 40, 1], [2, 25, 31], 8, 2, 64, 16, False, seed=15)
     _check(p, _call(p, window=window), window=min(window, 10 ** 6))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("new,kv,heads,kv_heads,dim,page,window,key", [
+    ([3, 2], [40, 9], 4, 1, 64, 16, 0, 38),
+    ([3, 2], [40, 9], 4, 1, 128, 16, 0, 39),
+    ([4, 1], [300, 70], 4, 2, 128, 16, 100, 198),
+    ([40, 5], [40, 20], 8, 2, 128, 16, 0, 17),
+    ([40, 5], [40, 20], 8, 2, 64, 16, 0, 31),
+    ([70], [700], 8, 2, 64, 64, 0, 650),
+    ([70, 1], [400, 3], 8, 1, 128, 32, 90, 300),
+    ([260], [300], 16, 16, 128, 16, 50, 250),
+])
+def test_paged_attention_non_finite_rows_stay_with_those_who_see_them(new, kv, heads, kv_heads,
+                                                                      dim, page, window, key, q8):
+    """NaN and infinities in a value row reach the rows that see its key, in
+    their dims, and NaN in a key row the rows that see it: no others."""
+    p = _problem(new, kv, heads, kv_heads, dim, page, q8, seed=21)
+    at = (int(p["table"][0, key // page]), key % page)
+    pos = np.concatenate([np.arange(n) + m - n for n, m in zip(new, kv)])
+    first = np.arange(sum(new)) < new[0]
+    sees = first & (key <= pos) & ((pos - key < window) if window else True)
+    assert sees.any() and not sees.all()
+    nan8 = torch.tensor([0x7F], dtype=torch.uint8, device=DEV)
+
+    def poison(c, dims, value):
+        if q8:
+            c.view(torch.uint8)[at[0], :, at[1], dims] = nan8
+        else:
+            c[at[0], :, at[1], dims] = value
+
+    def check(out, dims):
+        k, v = _stored(p["cache"])
+        k, v = np.nan_to_num(k, nan=0.0, posinf=0.0, neginf=0.0), np.nan_to_num(
+            v, nan=0.0, posinf=0.0, neginf=0.0)
+        ref, mag = OL.paged_attention(_f64(p["q"]), k, v, p["table"].numpy(), p["cu"].tolist(),
+                                      p["kv"].tolist(), window=window)
+        got = _f64(out)
+        hit = np.zeros(got.shape, bool)
+        hit[np.ix_(np.flatnonzero(sees), np.arange(heads), dims)] = True
+        assert not np.isfinite(got[hit]).any()
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * mag
+        bad = ~hit & ~(np.abs(got - ref) <= tol)
+        assert not bad.any(), f"{int(bad.sum())} values off, first {np.argwhere(bad)[0].tolist()}"
+
+    clean = [c.clone() if c is not None else None for c in p["cache"]]
+    for value in (float("nan"), float("inf"), float("-inf")):
+        poison(p["cache"][1], slice(5, dim - 3), value)
+        check(_call(p, window=window), np.arange(5, dim - 3))
+    p["cache"] = tuple(clean)
+    poison(p["cache"][0], slice(7, 9), float("nan"))
+    check(_call(p, window=window), np.arange(dim))
