@@ -2,8 +2,11 @@
 stream, the paged key/value cache and attention over it (include/bitdelta.h).
 
 Argument checks and marshalling only, as in bitdelta.py.  These calls are made
-for single tokens too, where the host's time counts, so the checks are kept to
-a few attribute reads and say what is wrong only once something is.
+for single tokens too, where the host's time is most of a call's (a launch by
+itself takes it 3.7 us), so each asks in one expression whether its tensors are
+as they usually are, and looks at them one by one, for what to allow or to
+refuse, only where they are not.  Outputs come from empty_like and new_empty,
+which read no keywords (1.2 and 1.4 us against 1.7 of torch.empty).
 """
 
 from __future__ import annotations
@@ -18,8 +21,9 @@ from . import bitdelta as _bd
 _BF16, _I32 = torch.bfloat16, torch.int32
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_current = torch.cuda.current_device
+_current = torch._C._cuda_getDevice
 _NONE = contextlib.nullcontext()
+_ROWS = torch.contiguous_format
 
 
 def _device(t, name: str) -> int:
@@ -58,61 +62,80 @@ def _at(dev: int, stream):
 
 # ------------------------------------------------------------------ norm
 def _rows(t, name: str, shape, dev: int):
-    """(pointer, stride) of the rows of a bf16 tensor [..., cols]: any row
-    stride in two dimensions, contiguous otherwise."""
+    """The stride of the rows of a bf16 tensor [..., cols]: any in two
+    dimensions, that of contiguous rows otherwise."""
     _is(t, name, _BF16, dev, contiguous=False)
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have x's shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
-        return t.data_ptr(), t.shape[-1]
+        return t.shape[-1]
     if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
-    return t.data_ptr(), t.stride(0)
+    return t.stride(0)
 
 
-def _norm(x, weight, eps, residual, y, h, stream, mx):
+def _norm_checks(x, weight, residual, y, h, mx):
+    """(x stride, residual stride) of tensors that are not all contiguous, or
+    what is wrong with them."""
     dev = _device(x, "x")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be [..., cols]")
     shape, cols = x.shape, x.shape[-1]
     if mx and cols % 32:
         raise ValueError(f"cols must be a multiple of 32 for an 8-bit output, got {cols}")
-    xp, xs = _rows(x, "x", None, dev)
+    xs = _rows(x, "x", None, dev)
     _is(weight, "weight", _BF16, dev)
     if weight.numel() != cols:
         raise ValueError(f"weight must hold {cols} elements, got {weight.numel()}")
-    rp = rs = 0
+    rs = 0
     if residual is not None:
-        rp, rs = _rows(residual, "residual", shape, dev)
+        rs = _rows(residual, "residual", shape, dev)
     elif h is not None:
         raise ValueError("h is written with a residual only")
+    for t, name in ((y, "y"), (h, "h")):
+        if t is not None:
+            _is(t, name, _BF16, dev)
+            if t.shape != shape:
+                raise ValueError(f"{name} must have x's shape")
+    return xs, rs
+
+
+def _norm(x, weight, eps, residual, y, h, stream, mx):
+    try:
+        shape = x.shape
+        xs = rs = cols = shape[-1]
+        dev = x.get_device()
+        usual = (cols > 0 and dev >= 0 and x.dtype is _BF16 and x.is_contiguous() and
+                 weight.dtype is _BF16 and weight.get_device() == dev and
+                 weight.numel() == cols and weight.is_contiguous() and
+                 y is None and h is None and not (mx and cols % 32) and
+                 (residual is None or residual.dtype is _BF16 and residual.shape == shape and
+                  residual.get_device() == dev and residual.is_contiguous()))
+    except (AttributeError, IndexError):
+        usual = False
+    if not usual:
+        xs, rs = _norm_checks(x, weight, residual, y, h, mx)
     with _at(dev, stream):
-        scale = None
-        if y is None:
-            y = torch.empty(shape, dtype=_E4M3 if mx else _BF16, device=x.device)
-        else:
-            _is(y, "y", _E4M3 if mx else _BF16, dev)
-            if y.shape != shape:
-                raise ValueError("y must have x's shape")
         if mx:
-            scale = torch.empty((*shape[:-1], cols // 32), dtype=_E8M0, device=x.device)
+            y = x.new_empty(shape, dtype=_E4M3)
+            scale = x.new_empty((*shape[:-1], cols // 32), dtype=_E8M0)
+        elif y is None:
+            y = torch.empty_like(x, memory_format=_ROWS)
+        rp = hp = None
         if residual is not None:
+            rp = residual.data_ptr()
             if h is None:
-                h = torch.empty(shape, dtype=_BF16, device=x.device)
-            else:
-                _is(h, "h", _BF16, dev)
-                if h.shape != shape:
-                    raise ValueError("h must have x's shape")
+                h = torch.empty_like(x, memory_format=_ROWS)
+            hp = h.data_ptr()
         rows = x.numel() // cols
         if mx:
             st = _bd.lib().bitdelta_rms_norm_mx(
-                xp, xs, rp or None, rs, weight.data_ptr(), eps, rows, cols,
-                None if h is None else h.data_ptr(), y.data_ptr(), scale.data_ptr(),
-                _raw_stream(dev))
+                x.data_ptr(), xs, rp, rs, weight.data_ptr(), eps, rows, cols, hp, y.data_ptr(),
+                scale.data_ptr(), _raw_stream(dev))
         else:
             st = _bd.lib().bitdelta_rms_norm(
-                xp, xs, rp or None, rs, weight.data_ptr(), eps, rows, cols,
-                None if h is None else h.data_ptr(), y.data_ptr(), _raw_stream(dev))
+                x.data_ptr(), xs, rp, rs, weight.data_ptr(), eps, rows, cols, hp, y.data_ptr(),
+                _raw_stream(dev))
     if st:
         _fail(st, "bitdelta_rms_norm_mx" if mx else "bitdelta_rms_norm")
     return (y, scale, h) if mx else (y, h)
@@ -133,8 +156,8 @@ def rms_norm_mx(x: torch.Tensor, weight: torch.Tensor, eps: float, residual=None
 
 
 # ------------------------------------------------------------------ cache
-def _cache(k_cache, v_cache, k_scale, v_scale, dev: int):
-    """(pages, heads, page, dim, k_scale pointer, v_scale pointer) of a cache."""
+def _cache_checks(k_cache, v_cache, k_scale, v_scale, dev: int):
+    """What is wrong with a cache."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a tensor [pages, heads, page, dim]")
     q8 = k_cache.dtype is _E4M3
@@ -144,33 +167,68 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dev: int):
     shape = k_cache.shape
     if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be of one shape")
-    pages, heads, page, dim = shape
-    if dim not in (64, 128) or page % 16 or not 16 <= page <= 65536 or pages < 1:
-        raise ValueError("a cache has dim 64 or 128 and pages of a multiple of 16 rows, "
-                         f"got {tuple(shape)}")
     if not q8:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache has no scales")
-        return pages, heads, page, dim, None, None
-    if k_scale is None or v_scale is None:
+    elif k_scale is None or v_scale is None:
         raise ValueError("an e4m3 cache needs k_scale and v_scale")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _is(t, name, _E8M0, dev)
-        if t.shape != shape[:3]:
-            raise ValueError(f"{name} must be [pages, heads, page]")
+    else:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _is(t, name, _E8M0, dev)
+            if t.shape != shape[:3]:
+                raise ValueError(f"{name} must be [pages, heads, page]")
+    raise ValueError("a cache has dim 64 or 128 and pages of a multiple of 16 rows, "
+                     f"got {tuple(shape)}")
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, dev: int):
+    """(pages, heads, page, dim, k_scale pointer, v_scale pointer) of a cache."""
+    try:
+        shape, kind = k_cache.shape, k_cache.dtype
+        pages, heads, page, dim = shape
+        good = (v_cache.dtype is kind and v_cache.shape == shape and
+                k_cache.get_device() == dev and v_cache.get_device() == dev and
+                k_cache.is_contiguous() and v_cache.is_contiguous() and
+                (dim == 128 or dim == 64) and not page % 16 and 16 <= page <= 65536 and
+                pages > 0 and
+                (k_scale is None and v_scale is None if kind is _BF16 else
+                 kind is _E4M3 and k_scale.dtype is _E8M0 and v_scale.dtype is _E8M0 and
+                 k_scale.get_device() == dev and v_scale.get_device() == dev and
+                 k_scale.shape == v_scale.shape == (pages, heads, page) and
+                 k_scale.is_contiguous() and v_scale.is_contiguous()))
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        _cache_checks(k_cache, v_cache, k_scale, v_scale, dev)
+    if k_scale is None:
+        return pages, heads, page, dim, None, None
     return pages, heads, page, dim, k_scale.data_ptr(), v_scale.data_ptr()
 
 
 def _heads(t, name: str, dev: int, heads, dim: int):
-    """A bf16 [tokens, heads, dim] view with contiguous dims."""
+    """The strides of a bf16 [tokens, heads, dim] view with contiguous dims."""
+    try:
+        shape, s = t.shape, t.stride()
+        if (t.dtype is _BF16 and t.get_device() == dev and len(s) == 3 and s[2] == 1 and
+                shape[2] == dim and (heads is None or shape[1] == heads)):
+            return s
+    except AttributeError:
+        pass
     _is(t, name, _BF16, dev, contiguous=False)
     if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], "
                          f"got {tuple(t.shape)}")
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return s
+    raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def _ints(t, name: str, dev: int) -> int:
+    """The number of values of an int32 tensor."""
+    try:
+        if t.dtype is _I32 and t.get_device() == dev and t.is_contiguous():
+            return t.numel()
+    except AttributeError:
+        pass
+    _is(t, name, _I32, dev)
 
 
 def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
@@ -182,9 +240,8 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: tor
     pages, heads, page, dim, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     sk = _heads(k, "k", dev, heads, dim)
     sv = _heads(v, "v", dev, heads, dim)
-    _is(slots, "slots", _I32, dev)
-    tokens = k.shape[0]
-    if v.shape[0] != tokens or slots.numel() != tokens:
+    tokens = _ints(slots, "slots", dev)
+    if k.shape[0] != tokens or v.shape[0] != tokens:
         raise ValueError("k, v and slots must have one entry per token")
     with _at(dev, stream):
         st = _bd.lib().bitdelta_kv_write(
@@ -199,12 +256,11 @@ def kv_read(slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k
             v_scale=None, stream=None):
     """(k, v): the cache rows slots as bf16 [tokens, heads, dim]."""
     dev = _device(slots, "slots")
-    _is(slots, "slots", _I32, dev)
+    tokens = _ints(slots, "slots", dev)
     pages, heads, page, dim, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
-    tokens = slots.numel()
     with _at(dev, stream):
-        k = torch.empty((tokens, heads, dim), dtype=_BF16, device=slots.device)
-        v = torch.empty((tokens, heads, dim), dtype=_BF16, device=slots.device)
+        k = slots.new_empty((tokens, heads, dim), dtype=_BF16)
+        v = torch.empty_like(k)
         st = _bd.lib().bitdelta_kv_read(
             slots.data_ptr(), tokens, heads, dim, pages, page, k_cache.data_ptr(),
             v_cache.data_ptr(), ks, vs, k.data_ptr(), v.data_ptr(), _raw_stream(dev))
@@ -235,14 +291,12 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     dev = _device(q, "q")
     pages, kv_heads, page, dim, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     s = _heads(q, "q", dev, None, dim)
-    tokens, heads = q.shape[0], q.shape[1]
+    tokens, heads, _ = q.shape
     if heads % kv_heads or not 1 <= heads // kv_heads <= 64:
         raise ValueError(f"{heads} query heads do not share {kv_heads} key/value heads")
-    _is(table, "table", _I32, dev)
-    _is(cu_q, "cu_q", _I32, dev)
-    _is(kv_len, "kv_len", _I32, dev)
-    seqs = kv_len.numel()
-    if table.dim() != 2 or table.shape[0] != seqs or cu_q.numel() != seqs + 1:
+    seqs = _ints(kv_len, "kv_len", dev)
+    _ints(table, "table", dev)
+    if (_ints(cu_q, "cu_q", dev) != seqs + 1 or table.dim() != 2 or table.shape[0] != seqs):
         raise ValueError("table must be [seqs, width], cu_q [seqs + 1] and kv_len [seqs]")
     if window < 0 or max_q < 0:
         raise ValueError("window and max_q must not be negative")
@@ -250,7 +304,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     L = _bd.lib()
     with _at(dev, stream):
         if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=_BF16, device=q.device)
+            out = torch.empty_like(q, memory_format=_ROWS)
         else:
             _is(out, "out", _BF16, dev)
             if out.shape != q.shape:
@@ -260,7 +314,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             wn = L.bitdelta_paged_attention_workspace_size(tokens, seqs, max_q, heads, kv_heads,
                                                            dim, width, page)
             if wn:
-                workspace = torch.empty(wn, dtype=torch.uint8, device=q.device)
+                workspace = kv_len.new_empty((wn + 3) // 4)
                 wp = workspace.data_ptr()
         else:
             if workspace.get_device() != dev or not workspace.is_contiguous():
