@@ -87,10 +87,10 @@ __device__ __forceinline__ float scale_of(uint32_t dword, int r) {
 // The lengths lie on the device, so every workgroup finds its own work: item
 // index -> (sequence b, tile, piece of the tile's keys, key/value head), heads
 // fastest, pieces next.  A sequence whose widest tile has `blocks` blocks of
-// 32 keys is cut into ceil(blocks / C) pieces a tile, with C such that all
-// items together are about `round` or `target`; each piece takes an equal share of its
-// own tile's blocks.  Then items <= target + tiles * kv_heads, which bounds
-// the grid and the workspace on the host.  Every wave computes the same plan
+// 32 keys is cut into ceil(blocks / C - part) pieces a tile, with C such that
+// all items together are about `round` or `target`; each piece takes an equal
+// share of its own tile's blocks.  Then items <= target + tiles * kv_heads,
+// which bounds the grid and the workspace on the host.  Every wave computes the same plan
 // (lane by sequence, 64 at a time), and the joining kernel again.
 struct Cut {
   int R;                       // rows a tile
@@ -98,6 +98,7 @@ struct Cut {
   int min_blocks, enough;      // blocks a piece: at least; for more than one round
   int least, most;             // rows (n * group) of the sequences taken: least < rows <= most
   float share;                 // kv_heads / round; 0: nothing is cut
+  float part;                  // a rest of this part of a piece or less joins its neighbours
 };
 
 struct Item {
@@ -131,15 +132,22 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Cut& c, int i
   const bool many = a.seqs > 64;
   Seq s{};
   float load = 0.f;
+  int longest = 0;
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
     float mine = 0.f;
+    int blocks = 0;
     if (b0 + lane < a.seqs) {
       s = seq_of(a, c, b0 + lane);
       mine = (float)s.tiles * (float)s.blocks;
+      blocks = s.tiles ? s.blocks : 0;
     }
     if (c.share == 0.f) break;
 #pragma unroll 1
-    for (int o = a.seqs > 1 ? 32 : 0; o > 0; o >>= 1) mine += __shfl_xor(mine, o);
+    for (int o = a.seqs > 1 ? 32 : 0; o > 0; o >>= 1) {
+      mine += __shfl_xor(mine, o);
+      if (JOIN) blocks = max(blocks, __shfl_xor(blocks, o));
+    }
+    if (JOIN) longest = max(longest, __builtin_amdgcn_readfirstlane(blocks));
     load += __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(mine)));
   }
   // One round of the card for little work, four for more: their ends differ by
@@ -148,12 +156,16 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Cut& c, int i
   const float C = fmaxf(floorf(fmaxf(fminf(one, (float)c.enough), four)) + 1.f,
                         (float)c.min_blocks);
   const float per_C = 1.f / C;
+  auto pieces_of = [&](int blocks) {
+    return max((int)fmaf((float)(blocks - 1), per_C, -c.part) + 1, 1);
+  };
+  if (JOIN && pieces_of(longest) == 1) return false;   // nothing was cut
   int before = 0, first = 0;   // tiles (JOIN) or items of the chunks before; items of them
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
     int pieces = 1, items = 0, tl = 0;
     if (b0 + lane < a.seqs) {
       if (many) s = seq_of(a, c, b0 + lane);
-      if (c.share != 0.f) pieces = max((int)((float)(s.blocks - 1) * per_C) + 1, 1);
+      if (c.share != 0.f) pieces = pieces_of(s.blocks);
       items = s.tiles * pieces;
       tl = s.tiles;
     }
@@ -214,49 +226,74 @@ __device__ __forceinline__ float* ml_at(const AttnArgs& a, const Cut& c, int D, 
   return a.partial + (size_t)a.items * c.R * D + (size_t)item * c.R * 2;
 }
 
-// One wave a row: the row's pieces added up, in the order of their keys.  A
-// workgroup takes 16 rows of a tile and head (4 of the tiles of 16).
+// Both launches' pieces: those of cut k in workgroups from[k] on.
+struct Join {
+  Cut cut[2];
+  float* partial[2];
+  int items[2], from1;
+};
+
+// A row's sums are held by D / 4 neighbouring lanes, four dims each; a
+// workgroup has 16 rows of a tile and head.  Eight pieces are read at once
+// (what a call waits for here is the memory's latency, not its rate).  The
+// order of the additions is that of the plan, which the lengths alone decide.
 template <int D>
-__global__ __launch_bounds__(256) void join_pieces_kernel(const AttnArgs a, const Cut c) {
-  const int rows = c.R == 16 ? 4 : 16, per = c.R / rows;   // powers of two
+__global__ __launch_bounds__(4 * D) void join_pieces_kernel(AttnArgs a, const Join j) {
+  const int which = (int)blockIdx.x >= j.from1;
+  const Cut c = j.cut[which];
+  a.partial = j.partial[which];
+  a.items = j.items[which];
+  const int idx = (int)blockIdx.x - (which ? j.from1 : 0), per = c.R / 16;   // powers of two
   Item it;
-  if (!find_item<true>(a, c, blockIdx.x / per, it) || it.pieces == 1) return;
+  if (!find_item<true>(a, c, idx / per, it) || it.pieces == 1) return;
   // cu_q that does not rise could ask for more items than there are
   if ((it.first + it.pieces) * a.kv_heads > a.items) return;
-  const int lane = threadIdx.x & 63;
+  const int row = (idx & (per - 1)) * 16 + threadIdx.x / (D / 4);
+  const int d0 = threadIdx.x % (D / 4) * 4;
+  const int r = it.tile * c.R + row;
+  if (r >= it.n * a.group) return;
   const int item0 = it.first * a.kv_heads + it.head;
-  for (int k = threadIdx.x >> 6; k < rows; k += 4) {
-    const int row = (blockIdx.x & (per - 1)) * rows + k;
-    const int r = it.tile * c.R + row;
-    if (r >= it.n * a.group) return;
-    float top = -INFINITY;
-    for (int p = lane; p < it.pieces; p += 64)
-      top = fmaxf(top, ml_at(a, c, D, item0 + p * a.kv_heads)[row * 2]);
+  float top = -INFINITY, tot = 0.f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  constexpr int U = 8;
+#pragma unroll 1
+  for (int p0 = 0; p0 < it.pieces; p0 += U) {
+    float m[U], l[U];
+    f32x4 s[U];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    constexpr int N = D / 64;
-    float tot = 0.f, v[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = 0.f;
-#pragma unroll 8
-    for (int p = 0; p < it.pieces; ++p) {
-      const int item = item0 + p * a.kv_heads;
-      const float* ml = ml_at(a, c, D, item) + row * 2;
-      const float f = __builtin_amdgcn_exp2f(ml[0] - ref);
-      tot = fmaf(f, ml[1], tot);
-      const float* s = sums_at(a, c, D, item) + (size_t)row * D + lane * N;
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = fmaf(f, s[e], v[e]);
+    for (int u = 0; u < U; ++u) {
+      m[u] = -INFINITY;
+      l[u] = 0.f;
+      s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (p0 + u < it.pieces) {
+        const int item = item0 + (p0 + u) * a.kv_heads;
+        const float* ml = ml_at(a, c, D, item) + row * 2;
+        m[u] = ml[0];
+        l[u] = ml[1];
+        s[u] = *reinterpret_cast<const f32x4*>(sums_at(a, c, D, item) + (size_t)row * D + d0);
+      }
     }
-    const float inv = tot == 0.f ? 0.f : 1.f / tot;
-    const int i = a.by_group.of(r);
-    uint16_t* o =
-        a.out + ((int64_t)(it.q0 + i) * a.heads + it.head * a.group + r - i * a.group) * D +
-        lane * N;
+    float next = top;
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = f32_to_bf16_bits(v[e] * inv);
+    for (int u = 0; u < U; ++u) next = fmaxf(next, m[u]);
+    const float ref = next == -INFINITY ? 0.f : next;
+    const float old = __builtin_amdgcn_exp2f(top - ref);
+    top = next;
+    tot *= old;
+    v *= old;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float f = __builtin_amdgcn_exp2f(m[u] - ref);
+      tot = fmaf(f, l[u], tot);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = fmaf(f, s[u][e], v[e]);
+    }
   }
+  v *= tot == 0.f ? 0.f : 1.f / tot;
+  const int i = a.by_group.of(r);
+  uint16_t* o =
+      a.out + ((int64_t)(it.q0 + i) * a.heads + it.head * a.group + r - i * a.group) * D + d0;
+  *reinterpret_cast<u32x2*>(o) = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
 }
 
 // ------------------------------------------------------------------ NaN, infinities
@@ -1082,7 +1119,7 @@ int64_t most_tiles(const AttnArgs& a, int R) {
 struct Way {
   Cut cut[2];        // few rows, many rows; R = 0: no such sequences
   int items[2];      // grids
-  size_t bytes;      // workspace
+  size_t bytes[2];   // workspaces
 };
 
 // Items that the plan can have at most.
@@ -1094,12 +1131,12 @@ Way way_of(const AttnArgs& a) {
   Way w{};
   const int64_t rows = (int64_t)a.max_q * a.group;
   const int kAll = 2147483647;
-  w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 256, 1024, 4, 16, 0, 16, 0.f};
+  w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 256, 1024, 4, 16, 0, 16, 0.f, 0.f};
   if (rows > 16) {
     const int64_t all = (int64_t)a.tokens * a.group;
     const int R = all / 128 * a.kv_heads >= 200 && all / a.seqs >= 128 ? 128 : 64;
     if (a.seqs == 1) w.cut[0].R = 0;   // one sequence: one launch, whatever its length
-    w.cut[1] = Cut{R, 512, 512, 8, 64, w.cut[0].R ? 16 : 0, kAll, 0.f};
+    w.cut[1] = Cut{R, 512, 512, 8, 64, w.cut[0].R ? 16 : 0, kAll, 0.f, 0.5f};
   }
   for (int k = 0; k < 2; ++k) {
     Cut& c = w.cut[k];
@@ -1112,10 +1149,7 @@ Way way_of(const AttnArgs& a) {
     AttnArgs b = a;
     if (k == 0 && rows > 16) b.max_q = 16 / a.group;
     w.items[k] = (int)most_items(b, c);
-    if (may) {
-      const size_t n = (size_t)w.items[k] * c.R * (a.dim + 2) * sizeof(float);
-      if (n > w.bytes) w.bytes = n;
-    }
+    if (may) w.bytes[k] = (size_t)w.items[k] * c.R * (a.dim + 2) * sizeof(float);
   }
   return w;
 }
@@ -1126,22 +1160,28 @@ hipError_t run(AttnArgs a, hipStream_t s) {
   a.by_page = divisor(a.page);
   a.by_heads = divisor(a.kv_heads);
   const Way w = way_of(a);
-  // the launches follow each other on the stream and share the workspace
+  Join j{};
+  int joins[2] = {0, 0};
   for (int k = 1; k >= 0; --k) {
     const Cut& c = w.cut[k];
     if (!c.R) continue;
-    a.items = w.items[k];
+    AttnArgs b = a;
+    b.items = w.items[k];
+    b.partial = a.partial + (k ? w.bytes[0] / sizeof(float) : 0);
     if (c.R == 16)
-      attend_rows16_kernel<D, Q8, 4, 2><<<a.items, 256, 0, s>>>(a, c);
+      attend_rows16_kernel<D, Q8, 4, 2><<<b.items, 256, 0, s>>>(b, c);
     else if (c.R == 64)
-      attend_many_kernel<D, Q8, 2><<<a.items, 256, 0, s>>>(a, c);
+      attend_many_kernel<D, Q8, 2><<<b.items, 256, 0, s>>>(b, c);
     else
-      attend_many_kernel<D, Q8, 4><<<a.items, 256, 0, s>>>(a, c);
-    if (c.share != 0.f) {
-      const int64_t joins = (a.items - c.target - 8) * (int64_t)(c.R == 16 ? 4 : c.R / 16);
-      join_pieces_kernel<D><<<(unsigned)joins, 256, 0, s>>>(a, c);
-    }
+      attend_many_kernel<D, Q8, 4><<<b.items, 256, 0, s>>>(b, c);
+    j.cut[k] = c;
+    j.partial[k] = b.partial;
+    j.items[k] = b.items;
+    if (c.share != 0.f) joins[k] = (b.items - c.target - 8) * (c.R / 16);
   }
+  j.from1 = joins[0];
+  if (joins[0] + joins[1] > 0)
+    join_pieces_kernel<D><<<(unsigned)(joins[0] + joins[1]), 4 * D, 0, s>>>(a, j);
   return hipGetLastError();
 }
 
@@ -1154,7 +1194,10 @@ Divisor divisor(int by) {
   return d;
 }
 
-size_t paged_attention_workspace(const AttnArgs& a) { return way_of(a).bytes; }
+size_t paged_attention_workspace(const AttnArgs& a) {
+  const Way w = way_of(a);
+  return w.bytes[0] + w.bytes[1];
+}
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t s) {
   const bool q8 = a.scale[0] != nullptr;
