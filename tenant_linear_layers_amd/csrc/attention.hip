@@ -22,6 +22,8 @@
 // as V^T has the same keys in the same places.  P therefore goes from one
 // product into the other without leaving its lane, and the running maximum
 // and sum of a query are held per lane.
+#include <type_traits>
+
 #include "common.h"
 #include "e4m3.h"
 #include "layer.h"
@@ -344,23 +346,23 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(BD_LDS const char*)p;
 }
 
-// Blocks of four rows at four addresses and OFF bytes after each.
-template <int OFF>
+// Blocks of four rows AT bytes after four addresses and OFF bytes on.
+template <int AT, int OFF>
 __device__ __forceinline__ void read_tr16(const uint32_t (&at)[4], u32x4 (&v)[4]) {
   u32x2 r[8];
   asm volatile(
-      "ds_read_b64_tr_b16 %0, %8\n"
-      "ds_read_b64_tr_b16 %1, %8 offset:%12\n"
-      "ds_read_b64_tr_b16 %2, %9\n"
-      "ds_read_b64_tr_b16 %3, %9 offset:%12\n"
-      "ds_read_b64_tr_b16 %4, %10\n"
-      "ds_read_b64_tr_b16 %5, %10 offset:%12\n"
-      "ds_read_b64_tr_b16 %6, %11\n"
-      "ds_read_b64_tr_b16 %7, %11 offset:%12\n"
+      "ds_read_b64_tr_b16 %0, %8 offset:%12\n"
+      "ds_read_b64_tr_b16 %1, %8 offset:%13\n"
+      "ds_read_b64_tr_b16 %2, %9 offset:%12\n"
+      "ds_read_b64_tr_b16 %3, %9 offset:%13\n"
+      "ds_read_b64_tr_b16 %4, %10 offset:%12\n"
+      "ds_read_b64_tr_b16 %5, %10 offset:%13\n"
+      "ds_read_b64_tr_b16 %6, %11 offset:%12\n"
+      "ds_read_b64_tr_b16 %7, %11 offset:%13\n"
       "s_waitcnt lgkmcnt(0)"
       : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]),
         "=&v"(r[6]), "=&v"(r[7])
-      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF)
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(AT), "n"(AT + OFF)
       : "memory");
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -369,10 +371,10 @@ __device__ __forceinline__ void read_tr16(const uint32_t (&at)[4], u32x4 (&v)[4]
 
 // Two tiles of dims, at[2 d] and at[2 d + 1] the blocks of rows k and k + 8:
 // v[2 d + c] has the rows 16 c + k and 16 c + k + 8, OFF = 16 rows.
-template <int OFF>
+template <int AT, int OFF>
 __device__ __forceinline__ void read_tr16_2x2(const uint32_t (&at)[4], u32x4 (&v)[4]) {
   u32x4 r[4];
-  read_tr16<OFF>(at, r);
+  read_tr16<AT, OFF>(at, r);
 #pragma unroll
   for (int d = 0; d < 2; ++d)
 #pragma unroll
@@ -600,7 +602,7 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
           at[e] = lds_address(
               vst + key * ROWB +
               (((2 * (d4 + e) + ((n >> 1) & 1)) ^ swizzle<ROWB>(key)) << 4) + 8 * (n & 1));
-        read_tr16<16 * ROWB>(at, vf);
+        read_tr16<0, 16 * ROWB>(at, vf);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[d4 + e] = mfma16(vf[e], pf, acc[d4 + e]);
@@ -724,6 +726,7 @@ template <int D, bool Q8, int RG>
 struct Many {
   static constexpr int KG = 4 / RG, R = 32 * RG;
   static constexpr int NB = Q8 || RG == 2 ? 2 : 4;
+  static constexpr int AHEAD = RG == 4 ? 2 : 1;      // e4m3: steps in registers
   static constexpr int ROWB = 2 * D;                 // in LDS
   static constexpr int STAGE = 32 * ROWB;            // 32 keys of K or V
   static constexpr int RING = 2 * NB * STAGE;        // K's, then V's
@@ -731,10 +734,14 @@ struct Many {
   static constexpr int SMEM = KG * RING > SUMS ? KG * RING : SUMS;
 };
 
+template <int I>
+using Step = std::integral_constant<int, I>;
+
 template <int D, bool Q8, int RG>
 __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, const Cut c) {
   using M = Many<D, Q8, RG>;
   constexpr int KG = M::KG, R = M::R, NB = M::NB, ROWB = M::ROWB, STAGE = M::STAGE;
+  constexpr int AHEAD = M::AHEAD;
   constexpr int SRC = Q8 ? D : 2 * D;                // bytes of a row in memory
   constexpr int P = SRC / 16;                        // its 16-byte pieces
   constexpr int KPI = 64 / P;                        // keys per load of a wave
@@ -785,65 +792,60 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
         bad |= key + 16 > lo;
     }
   };
-  // rows / 16 and valid keys of both halves of step i
+  // A wave's share of a step lies in one half of it: rows / 16 of the half and
+  // its valid keys, [below, keys).
+  const int half = MINE * rg / (LOADS / 2) & 1;
   struct Rows {
-    int blk[2], keys[2], below;
+    int blk, keys, below;
   };
   auto rows_of = [&](int i) {
     if ((i & 31) == 0) find_blocks(i);
     Rows r;
-    const int key0 = kbeg + 32 * KG * i;
-    r.below = lo - key0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int blk = __builtin_amdgcn_readlane(blocks, 2 * (i & 31) + h);
-      r.keys[h] = __builtin_amdgcn_readfirstlane(
-          blk < 0 || i >= steps ? 0 : min(max(hi - key0 - 16 * h, 0), 16));
-      r.blk[h] = max(blk, 0);
-    }
+    const int key0 = kbeg + 32 * KG * i + 16 * half;
+    const int blk = __builtin_amdgcn_readlane(blocks, 2 * (i & 31) + half);
+    // the same for the whole wave, which the compiler cannot see of all of it
+    r.below = __builtin_amdgcn_readfirstlane(lo - key0);
+    r.keys = __builtin_amdgcn_readfirstlane(
+        blk < 0 || i >= steps ? 0 : min(max(hi - key0, 0), 16));
+    r.blk = __builtin_amdgcn_readfirstlane(max(blk, 0));
     return r;
   };
 
-  // bf16: the wave's share of step i of K (w = 0) or V (1), straight into LDS
-  auto stage = [&](int w, int i, const Rows& r) {
-    char* st = (w ? vring : kring) + (i % NB) * STAGE;
+  // bf16: the wave's share of a step of K (w = 0) or V (1), straight into LDS
+  auto stage = [&](int w, int at, const Rows& r) {
+    char* st = (w ? vring : kring) + at * STAGE;
+    const uint8_t* src = a.cache[w] + (int64_t)r.blk * (16 * SRC);
 #pragma unroll
     for (int j = 0; j < MINE; ++j) {
-      const int load = rg + RG * j;                  // of the step's LOADS
-      const int h = load / (LOADS / 2);
+      const int load = MINE * rg + j;                // of the step's LOADS
       const int key = (load % (LOADS / 2)) * KPI + lane / P;   // of the half
       const int off = key * SRC + (((lane % P) ^ swizzle<ROWB>(key)) << 4);
-      lds_bload16(a.cache[w] + (int64_t)(h ? r.blk[1] : r.blk[0]) * (16 * SRC),
-                  (h ? r.keys[1] : r.keys[0]) * SRC, 16 * h + key < r.below ? 1 << 30 : off, 0,
-                  st + load * 1024);
+      lds_bload16(src, r.keys * SRC, key < r.below ? 1 << 30 : off, 0, st + load * 1024);
     }
   };
   // e4m3: the same rows and their scales into registers, then as bf16 into LDS
-  u32x4 raw[2][MINE];
-  uint32_t sc[2][MINE];
-  auto fetch = [&](int w, const Rows& r) {
+  u32x4 raw[AHEAD][2][MINE];
+  uint32_t sc[AHEAD][2][MINE];
+  auto fetch = [&](int w, int slot, const Rows& r) {
+    if (LOADS < RG * MINE && MINE * rg >= LOADS) return;
+    const int64_t at = (int64_t)r.blk * 16;
 #pragma unroll
     for (int j = 0; j < MINE; ++j) {
-      const int load = rg + RG * j;
-      if (LOADS % RG != 0 && load >= LOADS) break;
-      const int h = load / (LOADS / 2);
-      const int key = (load % (LOADS / 2)) * KPI + lane / P;
-      const bool below = 16 * h + key < r.below;
-      const int blk = h ? r.blk[1] : r.blk[0], keys = h ? r.keys[1] : r.keys[0];
-      raw[w][j] = bload128(a.cache[w] + (int64_t)blk * (16 * SRC), keys * SRC,
-                           below ? 1 << 30 : key * SRC + (lane % P) * 16, 0);
-      sc[w][j] = bload8(a.scale[w] + (int64_t)blk * 16, keys, below ? 1 << 30 : key, 0);
+      const int key = ((MINE * rg + j) % (LOADS / 2)) * KPI + lane / P;
+      const bool below = key < r.below;
+      raw[slot][w][j] = bload128(a.cache[w] + at * SRC, r.keys * SRC,
+                                 below ? 1 << 30 : key * SRC + (lane % P) * 16, 0);
+      sc[slot][w][j] = bload8(a.scale[w] + at, r.keys, below ? 1 << 30 : key, 0);
     }
   };
-  auto put = [&](int w, int i) {
-    char* st = (w ? vring : kring) + (i % NB) * STAGE;
+  auto put = [&](int w, int slot, int at) {
+    if (LOADS < RG * MINE && MINE * rg >= LOADS) return;
+    char* st = (w ? vring : kring) + at * STAGE;
 #pragma unroll
     for (int j = 0; j < MINE; ++j) {
-      const int load = rg + RG * j;
-      if (LOADS % RG != 0 && load >= LOADS) break;
-      const int key = load * KPI + lane / P;          // of the step
-      const float s = __uint_as_float(sc[w][j] << 23);
-      const u32x4 r = raw[w][j];
+      const int key = (MINE * rg + j) * KPI + lane / P;   // of the step
+      const float s = __uint_as_float(sc[slot][w][j] << 23);
+      const u32x4 r = raw[slot][w][j];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int piece = 2 * (lane % P) + e;
@@ -854,14 +856,15 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
     }
   };
 
-  f32x16 acc[D / 32];
+  f32x16 acc[D / 32], nil;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) nil[r] = 0.f;
   float m, l;
 
-  // one sixteen of the dims of the scores of step i
-  auto score = [&](int i, int s, f32x16& z) {
-    const u32x4 k4 = *reinterpret_cast<const u32x4*>(
-        kring + (i % NB) * STAGE + n * ROWB + (((2 * s + hh) ^ swizzle<ROWB>(n)) << 4));
-    z = mfma32(k4, qf[s], z);
+  // sixteen dims of K of a stage
+  auto keys = [&](int at, int s) {
+    return *reinterpret_cast<const u32x4*>(
+        kring + at * STAGE + n * ROWB + (((2 * s + hh) ^ swizzle<ROWB>(n)) << 4));
   };
 
   // Masks the scores of step i and moves the references.
@@ -895,30 +898,31 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
   auto weigh = [&](int r, float ref, f32x16& z, u32x4 (&pf)[2]) {
     const float p0 = __builtin_amdgcn_exp2f(fmaf(z[r], a.scale_log2, -ref));
     const float p1 = __builtin_amdgcn_exp2f(fmaf(z[r + 1], a.scale_log2, -ref));
-    l += p0;
-    l += p1;
-    pf[r >> 3][(r & 7) >> 1] = cvt_pk_bf16(p0, p1);
+    const uint32_t two = cvt_pk_bf16(p0, p1);
+    pf[r >> 3][(r & 7) >> 1] = two;
+    // the total is that of the weights as V sees them, rounded to bf16
+    l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two),
+                                        __builtin_bit_cast(bf16x2, 0x3F803F80u), l, false);
   };
 
   // V^T: lane (dim, hh) of tile d wants the rows 16 c + 4 hh + 0..3 and those
   // + 8; its 16 lanes read them at 4 rows x 32 bytes
-  int voff[D / 32][2];
+  uint32_t voff[D / 32][2];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int k = 8 * e + 4 * hh + ((lane & 15) >> 2);
       const int piece = 4 * d + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
-      voff[d][e] = k * ROWB + ((piece ^ swizzle<ROWB>(k)) << 4) + 8 * (lane & 1);
+      voff[d][e] = lds_address(vring) + k * ROWB + ((piece ^ swizzle<ROWB>(k)) << 4) +
+                   8 * (lane & 1);
     }
-  auto values = [&](int i, const u32x4 (&pf)[2]) {
-    const uint32_t st = lds_address(vring + (i % NB) * STAGE);
+  auto values = [&](auto at, const u32x4 (&pf)[2]) {
 #pragma unroll
     for (int d = 0; d < D / 32; d += 2) {
       u32x4 vf[4];
-      const uint32_t at[4] = {st + voff[d][0], st + voff[d][1], st + voff[d + 1][0],
-                              st + voff[d + 1][1]};
-      read_tr16_2x2<16 * ROWB>(at, vf);
+      const uint32_t four[4] = {voff[d][0], voff[d][1], voff[d + 1][0], voff[d + 1][1]};
+      read_tr16_2x2<at * STAGE, 16 * ROWB>(four, vf);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -949,69 +953,87 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
     m = -INFINITY;
     l = 0.f;
     if (steps > 0) {
-      f32x16 z, nil;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) nil[r] = 0.f;
-      Rows last;   // of the step that V is staged next
+      f32x16 z[2];
+      Rows last, coming;   // of the steps that V and K are staged of next
 #pragma unroll
       for (int i = 0; i < NB; ++i) {   // K of steps 0 .. NB - 1, V of 0 .. NB - 2
         last = rows_of(i);
         if (Q8) {
-          fetch(0, last);
-          put(0, i);
+          fetch(0, 0, last);
+          put(0, 0, i);
         } else {
           stage(0, i, last);
         }
         if (i == NB - 1) break;
         if (Q8) {
-          fetch(1, last);
-          put(1, i);
+          fetch(1, 0, last);
+          put(1, 0, i);
         } else {
           stage(1, i, last);
         }
       }
-      if (Q8) {
-        fetch(1, last);
-        last = rows_of(NB);
-        fetch(0, last);
+      coming = rows_of(NB);
+      if (Q8) {   // in registers: V of AHEAD steps from NB - 1 on, K from NB on
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+          fetch(1, (NB - 1 + k) % AHEAD, last);
+          fetch(0, (NB + k) % AHEAD, coming);
+          last = coming;
+          coming = rows_of(NB + k + 1);
+        }
       } else {
         wait_loads<0>();
       }
       wait_lds();
       meet();
-      z = nil;
+      z[0] = nil;
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) score(0, s, z);
-      for (int i = 0; i < steps; ++i) {
+      for (int s = 0; s < D / 16; ++s) z[0] = mfma32(keys(0, s), qf[s], z[0]);
+      // step i = u (mod NB): its scores are in now, those of i + 1 go to next
+      auto turn = [&](auto u, int i, f32x16& now, f32x16& next) {
         // K of step i + 1 and V of step i have arrived, and all waves have the
         // scores of step i and the values of step i - 1 behind them: K's stage
         // i and V's stage i - 1 may be written.
         if (!Q8) wait_loads<(NB - 2) * 2 * MINE>();
         wait_lds();
         meet();
+        u32x4 kf[D / 16];
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) kf[s] = keys((u + 1) % NB, s);
+        // the matrix products of one workgroup's wave go first, so that the
+        // other's softmax fills in
+        __builtin_amdgcn_s_setprio(1);
+        next = nil;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) next = mfma32(kf[s], qf[s], next);
         if (Q8) {
-          put(0, i + NB);
-          put(1, i + NB - 1);
-          fetch(1, last);
-          last = rows_of(i + NB + 1);
-          fetch(0, last);
+          put(0, u % AHEAD, u);
+          put(1, (u + NB - 1) % AHEAD, (u + NB - 1) % NB);
+          fetch(1, (u + NB - 1) % AHEAD, last);
+          fetch(0, u % AHEAD, coming);
         } else {
-          stage(1, i + NB - 1, last);
-          last = rows_of(i + NB);
-          stage(0, i + NB, last);
+          stage(1, (u + NB - 1) % NB, last);
+          stage(0, u, coming);
         }
-        look(i, z);
+        look(i, now);
         const float ref = m == -INFINITY ? 0.f : m;
-        f32x16 next = nil;
         u32x4 pf[2];
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          score(i + 1, s, next);
-#pragma unroll
-          for (int e = 0; e < 128 / D; ++e) weigh(2 * (s * (128 / D) + e), ref, z, pf);
+        for (int r = 0; r < 16; r += 2) weigh(r, ref, now, pf);
+        values(u, pf);
+        __builtin_amdgcn_s_setprio(0);
+        last = coming;
+        coming = rows_of(i + NB + 1 + (Q8 ? AHEAD : 0));
+      };
+      for (int i = 0; i < steps; i += NB) {
+        turn(Step<0>{}, i, z[0], z[1]);
+        // a turn past the last step finds no keys; without a branch here the
+        // rows on their way through registers need not arrive for a copy
+        if (Q8 || i + 1 < steps) turn(Step<1>{}, i + 1, z[1], z[0]);
+        if constexpr (NB == 4) {
+          if (i + 2 < steps) turn(Step<2>{}, i + 2, z[0], z[1]);
+          if (i + 3 < steps) turn(Step<3>{}, i + 3, z[1], z[0]);
         }
-        values(i, pf);
-        z = next;
       }
     }
     wait_loads<0>();
