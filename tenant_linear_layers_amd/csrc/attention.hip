@@ -340,47 +340,38 @@ __device__ __forceinline__ void query_range(const AttnArgs& a, const Tile& t, in
 // ------------------------------------------------------------------ reads of V
 // Transposing LDS reads: 16 lanes read 8 bytes each, together a block of four
 // rows of 16 bf16 (eight rows of 16 bytes), and lane n of them gets column n.
-// Several at once, their wait in the same statement: the builtins would also
-// wait for every load to LDS in flight, the next steps' among them.
+__device__ __forceinline__ u32x2 read_tr16(char* p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((BD_LDS s16x4*)p));
+}
+
+// Several at once, their wait in the same statement: under the 16-row kernel's
+// ring the builtin would also wait for every load to LDS in flight, the next
+// steps' among them.
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(BD_LDS const char*)p;
 }
 
-// Blocks of four rows AT bytes after four addresses and OFF bytes on.
-template <int AT, int OFF>
+// Blocks of four rows at four addresses and OFF bytes after each.
+template <int OFF>
 __device__ __forceinline__ void read_tr16(const uint32_t (&at)[4], u32x4 (&v)[4]) {
   u32x2 r[8];
   asm volatile(
-      "ds_read_b64_tr_b16 %0, %8 offset:%12\n"
-      "ds_read_b64_tr_b16 %1, %8 offset:%13\n"
-      "ds_read_b64_tr_b16 %2, %9 offset:%12\n"
-      "ds_read_b64_tr_b16 %3, %9 offset:%13\n"
-      "ds_read_b64_tr_b16 %4, %10 offset:%12\n"
-      "ds_read_b64_tr_b16 %5, %10 offset:%13\n"
-      "ds_read_b64_tr_b16 %6, %11 offset:%12\n"
-      "ds_read_b64_tr_b16 %7, %11 offset:%13\n"
+      "ds_read_b64_tr_b16 %0, %8\n"
+      "ds_read_b64_tr_b16 %1, %8 offset:%12\n"
+      "ds_read_b64_tr_b16 %2, %9\n"
+      "ds_read_b64_tr_b16 %3, %9 offset:%12\n"
+      "ds_read_b64_tr_b16 %4, %10\n"
+      "ds_read_b64_tr_b16 %5, %10 offset:%12\n"
+      "ds_read_b64_tr_b16 %6, %11\n"
+      "ds_read_b64_tr_b16 %7, %11 offset:%12\n"
       "s_waitcnt lgkmcnt(0)"
       : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]),
         "=&v"(r[6]), "=&v"(r[7])
-      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(AT), "n"(AT + OFF)
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(OFF)
       : "memory");
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     v[i] = u32x4{r[2 * i][0], r[2 * i][1], r[2 * i + 1][0], r[2 * i + 1][1]};
-}
-
-// Two tiles of dims, at[2 d] and at[2 d + 1] the blocks of rows k and k + 8:
-// v[2 d + c] has the rows 16 c + k and 16 c + k + 8, OFF = 16 rows.
-template <int AT, int OFF>
-__device__ __forceinline__ void read_tr16_2x2(const uint32_t (&at)[4], u32x4 (&v)[4]) {
-  u32x4 r[4];
-  read_tr16<AT, OFF>(at, r);
-#pragma unroll
-  for (int d = 0; d < 2; ++d)
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      v[2 * d + c] = u32x4{r[2 * d][2 * c], r[2 * d][2 * c + 1], r[2 * d + 1][2 * c],
-                           r[2 * d + 1][2 * c + 1]};
 }
 
 __device__ __forceinline__ void read_tr8(const uint32_t (&at)[4], u32x2 (&r)[4]) {
@@ -602,7 +593,7 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
           at[e] = lds_address(
               vst + key * ROWB +
               (((2 * (d4 + e) + ((n >> 1) & 1)) ^ swizzle<ROWB>(key)) << 4) + 8 * (n & 1));
-        read_tr16<0, 16 * ROWB>(at, vf);
+        read_tr16<16 * ROWB>(at, vf);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[d4 + e] = mfma16(vf[e], pf, acc[d4 + e]);
@@ -907,22 +898,28 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
 
   // V^T: lane (dim, hh) of tile d wants the rows 16 c + 4 hh + 0..3 and those
   // + 8; its 16 lanes read them at 4 rows x 32 bytes
-  uint32_t voff[D / 32][2];
+  char* voff[D / 32][2];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int k = 8 * e + 4 * hh + ((lane & 15) >> 2);
       const int piece = 4 * d + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
-      voff[d][e] = lds_address(vring) + k * ROWB + ((piece ^ swizzle<ROWB>(k)) << 4) +
+      voff[d][e] = vring + k * ROWB + ((piece ^ swizzle<ROWB>(k)) << 4) +
                    8 * (lane & 1);
     }
   auto values = [&](auto at, const u32x4 (&pf)[2]) {
 #pragma unroll
     for (int d = 0; d < D / 32; d += 2) {
       u32x4 vf[4];
-      const uint32_t four[4] = {voff[d][0], voff[d][1], voff[d + 1][0], voff[d + 1][1]};
-      read_tr16_2x2<at * STAGE, 16 * ROWB>(four, vf);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const u32x2 r = read_tr16(voff[d + (x >> 1)][x & 1] + at * STAGE + c * 16 * ROWB);
+          vf[(x & 2) + c][2 * (x & 1)] = r[0];
+          vf[(x & 2) + c][2 * (x & 1) + 1] = r[1];
+        }
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -1000,8 +997,8 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
         u32x4 kf[D / 16];
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) kf[s] = keys((u + 1) % NB, s);
-        // the matrix products of one workgroup's wave go first, so that the
-        // other's softmax fills in
+        // one workgroup's matrix products go first and the other's softmax
+        // fills in: without it 4% more time
         __builtin_amdgcn_s_setprio(1);
         next = nil;
 #pragma unroll
@@ -1015,11 +1012,13 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
           stage(1, (u + NB - 1) % NB, last);
           stage(0, u, coming);
         }
+        __builtin_amdgcn_s_setprio(0);
         look(i, now);
         const float ref = m == -INFINITY ? 0.f : m;
         u32x4 pf[2];
 #pragma unroll
         for (int r = 0; r < 16; r += 2) weigh(r, ref, now, pf);
+        __builtin_amdgcn_s_setprio(1);
         values(u, pf);
         __builtin_amdgcn_s_setprio(0);
         last = coming;
