@@ -96,7 +96,7 @@ __device__ __forceinline__ float scale_of(uint32_t dword, int r) {
 // (lane by sequence, 64 at a time), and the joining kernel again.
 struct Cut {
   int R;                       // rows a tile
-  int round, target;           // items of one round of the card; items aimed at
+  int round, target;           // items aimed at: of little work, of more
   int min_blocks, enough;      // blocks a piece: at least; for more than one round
   int least, most;             // rows (n * group) of the sequences taken: least < rows <= most
   float share;                 // kv_heads / round; 0: nothing is cut
@@ -1152,7 +1152,9 @@ Way way_of(const AttnArgs& a) {
   Way w{};
   const int64_t rows = (int64_t)a.max_q * a.group;
   const int kAll = 2147483647;
-  w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 256, 1024, 4, 16, 0, 16, 0.f, 0.f};
+  // 128 pieces of little work, not one a CU: their join is longer than what the
+  // other CUs would save (a token at 4097 keys 15.2 / 15.9 us, in 8 bits 14.1 / 15.0)
+  w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 128, 1024, 4, 16, 0, 16, 0.f, 0.f};
   if (rows > 16) {
     const int64_t all = (int64_t)a.tokens * a.group;
     const int R = all / 128 * a.kv_heads >= 200 && all / a.seqs >= 128 ? 128 : 64;
@@ -1181,6 +1183,11 @@ hipError_t run(AttnArgs a, hipStream_t s) {
   a.by_page = divisor(a.page);
   a.by_heads = divisor(a.kv_heads);
   const Way w = way_of(a);
+  // Waves of a workgroup of few rows: two rings of 64 KB at most fit a CU, and
+  // then the second workgroup's start and end lie under the first one's loads.
+  // bf16 rows of 128 dims with 2 / 4 waves: a token at 4097 keys 15.9 / 19.6
+  // us, 4 of them 22.7 / 28.1, 32 sequences of up to 16000 keys 163 / 160.
+  constexpr int NW = !Q8 && D == 128 ? 2 : 4;
   Join j{};
   int joins[2] = {0, 0};
   for (int k = 1; k >= 0; --k) {
@@ -1190,7 +1197,7 @@ hipError_t run(AttnArgs a, hipStream_t s) {
     b.items = w.items[k];
     b.partial = a.partial + (k ? w.bytes[0] / sizeof(float) : 0);
     if (c.R == 16)
-      attend_rows16_kernel<D, Q8, 4, 2><<<b.items, 256, 0, s>>>(b, c);
+      attend_rows16_kernel<D, Q8, NW, 2><<<b.items, NW * 64, 0, s>>>(b, c);
     else if (c.R == 64)
       attend_many_kernel<D, Q8, 2><<<b.items, 256, 0, s>>>(b, c);
     else
