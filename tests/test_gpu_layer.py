@@ -508,3 +508,62 @@ def test_paged_attention_non_finite_rows_stay_with_those_who_see_them(new, kv, h
     p["cache"] = tuple(clean)
     poison(p["cache"][0], slice(7, 9), float("nan"))
     check(_call(p, window=window), np.arange(dim))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("new,kv,heads,kv_heads,dim,page,window", [
+    ([1], [9000], 2, 1, 64, 16, 0),                          # more pieces than a join reads at once
+    ([1], [5000], 64, 1, 128, 64, 0),                        # one token of more rows than 16
+    ([1] * 150, [(37 * i) % 211 + 1 for i in range(150)], 4, 1, 64, 16, 0),
+    ([1] * 70, [(97 * i) % 900 + 1 for i in range(69)] + [6000], 2, 1, 128, 16, 0),
+    ([1 + i % 3 for i in range(130)], [(53 * i) % 300 + 3 for i in range(130)], 4, 2, 64, 32, 40),
+    ([40 * (i % 9 == 0) + i % 2 for i in range(100)],
+     [40 + (71 * i) % 400 for i in range(100)], 2, 1, 128, 16, 0),
+    ([300], [3000], 1, 1, 128, 16, 1700),
+])
+def test_paged_attention_long_and_many_sequences(new, kv, heads, kv_heads, dim, page, window, q8):
+    p = _problem(new, kv, heads, kv_heads, dim, page, q8, seed=31)
+    _check(p, _call(p, window=window), window=window)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_cache_rows_and_query_strides_past_32_bits(q8):
+    """Rows of a cache that lie beyond 2^32 bytes, queries beyond 2^31 elements."""
+    heads, page, dim = 8, 64, 128
+    pages = 2 ** 32 // (heads * page * dim * (1 if q8 else 2)) + 40
+    kind = torch.float8_e4m3fn if q8 else torch.bfloat16
+    cache = [torch.empty((pages, heads, page, dim), dtype=kind, device=DEV) for _ in range(2)]
+    cache += [torch.empty((pages, heads, page), dtype=torch.float8_e8m0fnu, device=DEV)
+              for _ in range(2)] if q8 else [None, None]
+    new, kv = [1, 40], [150, 90]
+    small = _problem(new, kv, 8, heads, dim, page, q8, seed=41)
+    table = pages - 1 - torch.arange(small["table"].numel(), dtype=torch.int32).view(
+        small["table"].shape)
+    for b, m in enumerate(kv):
+        def slots(t):
+            t = t[b].to(DEV)
+            j = torch.arange(m, device=DEV)
+            return (t[j // page] * page + j % page).int()
+        k, v = T.kv_read(slots(small["table"]), *small["cache"])
+        T.kv_write(k, v, slots(table), *cache)
+        k2, v2 = T.kv_read(slots(table), *cache)
+        assert torch.equal(k, k2) and torch.equal(v, v2)
+    want = _call(small)
+    _check(small, want)
+    assert torch.equal(_call(dict(small, cache=cache, table=table)), want)
+    stride = 2 ** 31 // 40 + 8
+    q = torch.empty(40 * stride + 8 * dim, dtype=torch.bfloat16, device=DEV)
+    q = q.as_strided((41, 8, dim), (stride, dim, 1))
+    q.copy_(small["q"])
+    assert torch.equal(_call(dict(small, q=q)), want)
+
+
+def test_rms_norm_of_more_than_2_to_31_values():
+    rows, cols = 2 ** 31 // 8192 + 3, 8192
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV)
+    x[-5:] = _randn((5, cols), 51, 1.4)
+    w = _randn((cols,), 52, 0.1) + 1.0
+    for call in (lambda x: T.rms_norm(x, w, EPS, x)[:2],
+                 lambda x: [t.view(torch.uint8) for t in T.rms_norm_mx(x, w, EPS)[:2]]):
+        for big, few in zip(call(x), call(x[-5:].clone())):
+            assert torch.equal(big[-5:], few)
