@@ -43,16 +43,11 @@ __device__ __forceinline__ void st_some(uint16_t* p, u32x4 v, int n) {
     if (e < n) p[e] = (uint16_t)(v[e >> 1] >> ((e & 1) << 4));
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
 // Sum over the T threads of a row (T = 64, or the whole workgroup).
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-  v = wave_sum(v);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   if (T == kWave) return v;
   if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -60,6 +55,30 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
   for (int i = 0; i < T / kWave; ++i) s += red[i];
   return s;
+}
+
+// 1 / sqrt(mean square + eps).  For an 8-bit output as the sum of two floats
+// (one Newton step, its products exact by fma), and x times it times w with
+// one rounding: next to a border of the group's scale three roundings fall to
+// the other side more often, and then the whole group has the other scale.
+struct Inv {
+  float hi, lo;
+};
+template <bool MX>
+__device__ __forceinline__ Inv inverse(float sum, int cols, float eps) {
+  const float a = sum / (float)cols + eps, r = rsqrtf(a);
+  if (!MX) return {r, 0.f};
+  const float t = a * r;
+  const float lo = 0.5f * r * fmaf(-fmaf(a, r, -t), r, fmaf(-t, r, 1.f));
+  return {r, fabsf(lo) < INFINITY ? lo : 0.f};
+}
+template <bool MX>
+__device__ __forceinline__ float scaled(float x, Inv i, float w) {
+  const float p = x * i.hi;
+  if (!MX) return p * w;
+  // below 2^-22 of the product; held, so that an infinite w gives infinity
+  const float rest = fmaf(x, i.lo, fmaf(x, i.hi, -p)) * w;
+  return fmaf(p, w, __builtin_amdgcn_fmed3f(rest, -1e32f, 1e32f));
 }
 
 // Eight values of one row: load x (+ residual), write h, keep float32.
@@ -91,13 +110,13 @@ __device__ __forceinline__ void load_sum(const uint16_t* x, const uint16_t* r, u
 // group of 32 and share its largest magnitude.
 template <bool MX>
 __device__ __forceinline__ void put(const NormArgs& a, int64_t row, int col, int n,
-                                    const float (&f)[8], float inv) {
+                                    const float (&f)[8], Inv inv) {
   const u32x4 w = n >= 8 ? ld8(a.w + col) : ld_some(a.w + col, n);
   float y[8];
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
-    y[2 * d] = f[2 * d] * inv * lo16(w[d]);
-    y[2 * d + 1] = f[2 * d + 1] * inv * hi16(w[d]);
+    y[2 * d] = scaled<MX>(f[2 * d], inv, lo16(w[d]));
+    y[2 * d + 1] = scaled<MX>(f[2 * d + 1], inv, hi16(w[d]));
   }
   if (!MX) {
     u32x4 o;
@@ -148,7 +167,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(const NormA
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(f[c][e], f[c][e], ss);
-  const float inv = rsqrtf(row_sum<T>(ss, red) / (float)a.cols + a.eps);
+  const Inv inv = inverse<MX>(row_sum<T>(ss, red), a.cols, a.eps);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int col = (c * T + t) * 8;
@@ -173,7 +192,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const NormArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
   }
-  const float inv = rsqrtf(row_sum<1024>(ss, red) / (float)a.cols + a.eps);
+  const Inv inv = inverse<MX>(row_sum<1024>(ss, red), a.cols, a.eps);
   for (int64_t col = threadIdx.x * 8; col < a.cols; col += 8192) {
     load_sum<RES>(x + col, r + col, h + col, (int)(a.cols - col), f);
     put<MX>(a, row, (int)col, (int)(a.cols - col), f, inv);
