@@ -199,6 +199,13 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const NormArgs a) {
   }
 }
 
+// Threads of a row, by its length.  A wave by itself needs no barrier (20000
+// rows of 512: 13.7 us, 256 threads 15.4); more than two groups a thread lose
+// loads in flight (8000 rows of 2048: 256 threads 21.0, a wave 23.1; 4096 rows
+// of 4096: 512 threads 21.3, a wave 22.3, one row 2.5 and 5.6; 1000 of 16384:
+// 1024 threads 23.7, 512 24.8).  A row of 8192 takes 1024 threads (one row 2.9
+// us, 512 threads 3.3), for many rows in 8 bits, where the arithmetic counts,
+// 512 (2021 rows 20.1, 1024 threads 21.3).
 template <bool RES, bool MX>
 hipError_t pick(const NormArgs& a, hipStream_t s) {
   const unsigned rows = (unsigned)a.rows;
@@ -209,7 +216,9 @@ hipError_t pick(const NormArgs& a, hipStream_t s) {
   else if (a.cols <= 2048)
     rms_norm_kernel<256, 1, RES, MX><<<rows, 256, 0, s>>>(a);
   else if (a.cols <= 4096)
-    rms_norm_kernel<256, 2, RES, MX><<<rows, 256, 0, s>>>(a);
+    rms_norm_kernel<512, 1, RES, MX><<<rows, 512, 0, s>>>(a);
+  else if (MX && a.cols <= 8192 && rows >= 256)
+    rms_norm_kernel<512, 2, RES, MX><<<rows, 512, 0, s>>>(a);
   else if (a.cols <= 8192)
     rms_norm_kernel<1024, 1, RES, MX><<<rows, 1024, 0, s>>>(a);
   else if (a.cols <= 16384)
