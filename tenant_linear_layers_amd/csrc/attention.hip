@@ -1135,7 +1135,7 @@ int64_t most_tiles(const AttnArgs& a, int R) {
 }
 
 // How a call is carried out: sequences of up to 16 rows on the 16-row kernel,
-// others on tiles of 64 or 256.  Both kinds in one call are two launches, each
+// others on tiles of 64 or 128.  Both kinds in one call are two launches, each
 // with a plan of its own sequences.
 struct Way {
   Cut cut[2];        // few rows, many rows; R = 0: no such sequences
@@ -1148,24 +1148,46 @@ int64_t most_items(const AttnArgs& a, const Cut& c) {
   return most_tiles(a, c.R) * a.kv_heads + (c.share != 0.f ? c.target + 8 : 0);
 }
 
+// Rows of a tile of many rows.  128 rows read half of what tiles of 64 read
+// and need not share a workgroup's keys out: 200 tokens over 8000 keys, 4 rows
+// a token, 53 us against 78 (8 bits, 128 dims; of 64 dims 44 against 55).  64
+// where
+// * the average sequence would leave 128 too empty (40 tokens, 160 rows: 31.4
+//   us against 33.4; of 64 dims 25.9 against 30.6), or
+// * the tiles of 128 are about one round of the card and their lengths differ,
+//   new tokens being about half or more of the keys: 2048 tokens of 32 heads 61 us
+//   against 66, of 64 dims 37 against 47 (of 64 heads, two rounds, 118 against
+//   92; 512 tokens, a quarter of a round, 29 against 24).
+int rows_a_tile(const AttnArgs& a) {
+  const int64_t all = (int64_t)a.tokens * a.group, each = all / a.seqs;
+  const bool filled = (each + 127) / 128 * 128 * 4 <= (each + 63) / 64 * 64 * 5;
+  const int64_t tiles = all / 128 * a.kv_heads;
+  const bool uneven = tiles >= 200 && tiles < 1000 &&
+                      (int64_t)a.max_q * 9 >= (int64_t)a.width * a.page * 4;
+  return filled && !uneven ? 128 : 64;
+}
+
 Way way_of(const AttnArgs& a) {
   Way w{};
   const int64_t rows = (int64_t)a.max_q * a.group;
   const int kAll = 2147483647;
   // 128 pieces of little work, not one a CU: their join is longer than what the
-  // other CUs would save (a token at 4097 keys 15.2 / 15.9 us, in 8 bits 14.1 / 15.0)
+  // other CUs would save (a token at 4097 keys 15.2 / 15.9 us, in 8 bits 14.1 /
+  // 15.0).  1024 of more: 768 and 2048 are within 1% for 64 sequences, 2048 is
+  // 13% slower for 32.
   w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 128, 1024, 4, 16, 0, 16, 0.f, 0.f};
   if (rows > 16) {
-    const int64_t all = (int64_t)a.tokens * a.group;
-    const int R = all / 128 * a.kv_heads >= 200 && all / a.seqs >= 128 ? 128 : 64;
+    w.cut[1] = Cut{rows_a_tile(a), 512, 512, 8, 64, 0, kAll, 0.f, 0.5f};
     if (a.seqs == 1) w.cut[0].R = 0;   // one sequence: one launch, whatever its length
-    w.cut[1] = Cut{R, 512, 512, 8, 64, w.cut[0].R ? 16 : 0, kAll, 0.f, 0.5f};
+    if (w.cut[0].R) w.cut[1].least = 16;
   }
   for (int k = 0; k < 2; ++k) {
     Cut& c = w.cut[k];
     if (!c.R) continue;
     // cut only where a tile can be longer than the shortest piece, and, for
-    // many rows, where the tiles by themselves do not fill the card
+    // many rows, where the tiles by themselves are not two rounds of the card
+    // (2048 tokens of 64 heads: 92 us, cut 107).  Pieces of 8 blocks or more:
+    // of 16 / 32, 24 mixed sequences take 36 / 40 us for 32.
     const bool may = ((int64_t)a.width * a.page + 31) / 32 + 1 > c.min_blocks &&
                      (k == 0 || (int64_t)a.tokens * a.group / c.R * a.kv_heads < 2 * c.target);
     c.share = may ? (float)a.kv_heads / (float)c.round : 0.f;
