@@ -6,7 +6,8 @@
 // tokens, by the launch.  dim / 8 neighbouring lanes hold a row: one 16-byte
 // access a lane on the bf16 side, and the row's largest magnitude by lane
 // exchanges, so a row needs no LDS.  Neighbouring rows of a token are its
-// heads, contiguous on the side of the tokens.
+// heads, contiguous on the side of the tokens.  64 tokens into 8 bits take 3.3
+// us, 2048 5.9 us, 16001 back 20.6 us (4.8 TB/s; a copy reaches 4.9).
 #include "common.h"
 #include "e4m3.h"
 #include "layer.h"
