@@ -89,18 +89,18 @@ __device__ __forceinline__ float scale_of(uint32_t dword, int r) {
 // The lengths lie on the device, so every workgroup finds its own work: item
 // index -> (sequence b, tile, piece of the tile's keys, key/value head), heads
 // fastest, pieces next.  A sequence whose widest tile has `blocks` blocks of
-// 32 keys is cut into ceil(blocks / C - part) pieces a tile, with C such that
-// all items together are about `round` or `target`; each piece takes an equal
-// share of its own tile's blocks.  Then items <= target + tiles * kv_heads,
-// which bounds the grid and the workspace on the host.  Every wave computes the same plan
-// (lane by sequence, 64 at a time), and the joining kernel again.
+// 32 keys is cut into about ceil(blocks / C - 1/2) pieces a tile, with C such
+// that all items together are about `round` or `target`; each piece takes an
+// equal share of its own tile's blocks.  Then items <= target + tiles *
+// kv_heads, which bounds the grid and the workspace on the host.  Every wave
+// computes the same plan (lane by sequence, 64 at a time), and the joining
+// kernel again.
 struct Cut {
   int R;                       // rows a tile
   int round, target;           // items aimed at: of little work, of more
   int min_blocks, enough;      // blocks a piece: at least; for more than one round
   int least, most;             // rows (n * group) of the sequences taken: least < rows <= most
   float share;                 // kv_heads / round; 0: nothing is cut
-  float part;                  // a rest of this part of a piece or less joins its neighbours
 };
 
 struct Item {
@@ -158,8 +158,10 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Cut& c, int i
   const float C = fmaxf(floorf(fmaxf(fminf(few, (float)c.enough), more)) + 1.f,
                         (float)c.min_blocks);
   const float per_C = 1.f / C;
+  // A rest of half a piece or less is none of its own: 32 sequences in bf16
+  // 151 us, with it 163 (64 in 8 bits 143 / 142; 24 mixed ones 32.5 / 33.9).
   auto pieces_of = [&](int blocks) {
-    return max((int)fmaf((float)(blocks - 1), per_C, -c.part) + 1, 1);
+    return max((int)fmaf((float)(blocks - 1), per_C, -0.5f) + 1, 1);
   };
   if (JOIN && pieces_of(longest) == 1) return false;   // nothing was cut
   int before = 0, first = 0;   // tiles (JOIN) or items of the chunks before; items of them
@@ -405,7 +407,7 @@ __device__ __forceinline__ void wait_lds() {
 // matrix operands, so there is no barrier until the waves' sums are joined.
 //
 // Bound by HBM: 64 sequences in 8 bits (688 MB) take 134 us, 5.1 TB/s, 32 in
-// bf16 (795 MB) 152 us, 5.2 TB/s (a copy reaches 4.9 on this card); the CUs
+// bf16 (795 MB) 142 us, 5.6 TB/s (a copy reaches 4.9 on this card); the CUs
 // stand idle a fifth of the time at the ends.  A single token at 4097 keys,
 // 10.4 us, is a chain of latencies: plan, page table, K, V, joins.
 template <int D, bool Q8, int NW, int U>
@@ -716,8 +718,8 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
 // wanted one step before V, and their two rings in LDS are NB steps deep each.
 //
 // A prompt of 2048 (64 heads of 128) takes 90 us, 760 TFLOP/s, a chunk of 509
-// over 16384 keys in 8 bits 306 us, 907 TFLOP/s; the matrix cores are busy 32%
-// and 39% of the time (rocprofv3).  What bounds it is the latency of a wave's
+// over 16384 keys in 8 bits 306 us, 907 TFLOP/s; the matrix cores are busy 33%
+// and 40% of the time (rocprofv3).  What bounds it is the latency of a wave's
 // step: one workgroup a CU takes twice the time, and no part left out (the
 // exponentials, the reads of K or V, the barrier) saves more than 5%.  The
 // registers (64 sums, 32 of Q, 32 scores a lane) allow two waves a SIMD.
@@ -1185,11 +1187,11 @@ Way way_of(const AttnArgs& a) {
   const int kAll = 2147483647;
   // 128 pieces of little work, not one a CU: their join is longer than what the
   // other CUs would save (a token at 4097 keys 15.2 / 15.9 us, in 8 bits 14.1 /
-  // 15.0).  1024 of more: 768 and 2048 are within 1% for 64 sequences, 2048 is
-  // 13% slower for 32.
-  w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 128, 1024, 4, 16, 0, 16, 0.f, 0.f};
+  // 15.0).  1024 of more: 32 sequences in bf16 151 us, 1280 158 us, 1536 154; 40
+  // sequences of 8000 keys 231, 242 and 254.
+  w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 128, 1024, 4, 16, 0, 16, 0.f};
   if (rows > 16) {
-    w.cut[1] = Cut{rows_a_tile(a), 512, 512, 8, 64, 0, kAll, 0.f, 0.5f};
+    w.cut[1] = Cut{rows_a_tile(a), 512, 512, 8, 64, 0, kAll, 0.f};
     if (a.seqs == 1) w.cut[0].R = 0;   // one sequence: one launch, whatever its length
     if (w.cut[0].R) w.cut[1].least = 16;
   }
