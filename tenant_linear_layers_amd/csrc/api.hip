@@ -566,6 +566,7 @@ BD_EXPORT size_t bitdelta_paged_attention_workspace_size(int64_t tokens, int64_t
                                                          int64_t kv_heads, int64_t dim,
                                                          int64_t width, int64_t page) {
   if (!attention_shape_ok(tokens, seqs, max_q, heads, kv_heads, dim, width, page)) return 0;
+  if (tokens == 0 || seqs == 0 || max_q == 0) return 0;   // nothing to do
   return bd::paged_attention_workspace(
       attention_sizes(tokens, seqs, max_q, heads, kv_heads, dim, width, page));
 }

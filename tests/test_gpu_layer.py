@@ -567,3 +567,13 @@ def test_rms_norm_of_more_than_2_to_31_values():
                  lambda x: [t.view(torch.uint8) for t in T.rms_norm_mx(x, w, EPS)[:2]]):
         for big, few in zip(call(x), call(x[-5:].clone())):
             assert torch.equal(big[-5:], few)
+
+
+def test_paged_attention_of_no_sequences_or_rows():
+    p = _problem([2, 1], [20, 20], 16, 1, 64, 16, False, seed=61)
+    q, c = p["q"], p["cache"]
+    t, cu, kv = p["table"].to(DEV), p["cu"].to(DEV), p["kv"].to(DEV)
+    out = torch.full_like(q, 3.0)
+    for args in ((t[:0], cu[:1], kv[:0], 2), (t, cu, kv, 0)):
+        assert T.paged_attention(q, c[0], c[1], *args, out=out) is out
+        assert bool((out == 3.0).all())                     # rows that no sequence has

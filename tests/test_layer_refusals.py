@@ -101,6 +101,18 @@ def test_paged_attention_refuses_sequences_past_2_to_30_keys():
              (1 << 26) + 1, 1.0, 0, E, F, 1 << 40, None) == 2
 
 
+def test_paged_attention_workspace_of_nothing():
+    """No sequences, tokens or rows: no workspace, whatever the other sizes."""
+    size = T.paged_attention_workspace_size
+    for tokens in (0, 1, 5000):
+        for seqs in (0, 3):
+            for max_q in (0, 1, 5000):
+                if tokens and seqs and max_q:
+                    continue
+                for heads, kv_heads in ((64, 8), (64, 1), (8, 8)):
+                    assert size(tokens, seqs, max_q, heads, kv_heads, 128, 300, 16) == 0
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.125, -0.0, 1e-40, math.inf, -math.inf, math.nan, 3e38])
 def test_paged_attention_refuses_scales_that_do_not_keep_the_scores_order(scale):
     f = T.lib().bitdelta_paged_attention
