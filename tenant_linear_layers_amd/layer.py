@@ -177,7 +177,7 @@ def _cache_checks(k_cache, v_cache, k_scale, v_scale, dev: int):
             _is(t, name, _E8M0, dev)
             if t.shape != shape[:3]:
                 raise ValueError(f"{name} must be [pages, heads, page]")
-    raise ValueError("a cache has dim 64 or 128 and pages of a multiple of 16 rows, "
+    raise ValueError("a cache has pages, heads, dim 64 or 128 and pages of a multiple of 16 rows, "
                      f"got {tuple(shape)}")
 
 
@@ -190,7 +190,7 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dev: int):
                 k_cache.get_device() == dev and v_cache.get_device() == dev and
                 k_cache.is_contiguous() and v_cache.is_contiguous() and
                 (dim == 128 or dim == 64) and not page % 16 and 16 <= page <= 65536 and
-                pages > 0 and
+                pages > 0 and heads > 0 and
                 (k_scale is None and v_scale is None if kind is _BF16 else
                  kind is _E4M3 and k_scale.dtype is _E8M0 and v_scale.dtype is _E8M0 and
                  k_scale.get_device() == dev and v_scale.get_device() == dev and

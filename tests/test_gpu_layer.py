@@ -577,3 +577,15 @@ def test_paged_attention_of_no_sequences_or_rows():
     for args in ((t[:0], cu[:1], kv[:0], 2), (t, cu, kv, 0)):
         assert T.paged_attention(q, c[0], c[1], *args, out=out) is out
         assert bool((out == 3.0).all())                     # rows that no sequence has
+
+
+def test_caches_of_no_heads_or_pages_are_refused():
+    s = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q = _randn((1, 4, 64), 62)
+    for shape in ((2, 0, 16, 64), (0, 2, 16, 64)):
+        c = torch.zeros(shape, dtype=torch.bfloat16, device=DEV)
+        with pytest.raises(ValueError):
+            T.kv_read(s, c, c.clone())
+        with pytest.raises(ValueError):
+            T.paged_attention(q, c, c.clone(), s.view(1, 1), torch.zeros(2, dtype=torch.int32,
+                                                                         device=DEV), s, 1)
