@@ -200,6 +200,33 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const NormArgs a) {
   }
 }
 
+// A launch takes fewer than 2^32 threads: more rows than that go in several,
+// of 2^31 threads each.
+constexpr int64_t kMostThreads = int64_t(1) << 31;
+
+template <int T, int CH, bool RES, bool MX>
+hipError_t rows_of(const NormArgs& a, hipStream_t s) {
+  constexpr int kBlock = T < 256 ? 256 : T, kRows = kBlock / T;   // of a workgroup
+  constexpr int64_t kMost = kMostThreads / T;
+  for (int64_t at = 0; at < a.rows; at += kMost) {
+    NormArgs b = a;
+    b.rows = a.rows - at < kMost ? a.rows - at : kMost;
+    b.x += at * a.x_stride;
+    if (RES) b.residual += at * a.r_stride;
+    if (RES) b.h += at * a.cols;
+    b.y = static_cast<uint8_t*>(a.y) + at * a.cols * (MX ? 1 : 2);
+    if (MX) b.scale += at * (a.cols >> 5);
+    const unsigned grid = (unsigned)((b.rows + kRows - 1) / kRows);
+    if constexpr (CH > 0)
+      rms_norm_kernel<T, CH, RES, MX><<<grid, kBlock, 0, s>>>(b);
+    else
+      rms_norm_long_kernel<RES, MX><<<grid, kBlock, 0, s>>>(b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // Threads of a row, by its length.  A wave by itself needs no barrier (20000
 // rows of 512: 13.7 us, 256 threads 15.4); more than two groups a thread lose
 // loads in flight (8000 rows of 2048: 256 threads 21.0, a wave 23.1; 4096 rows
@@ -209,24 +236,14 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const NormArgs a) {
 // 512 (2021 rows 20.1, 1024 threads 21.3).
 template <bool RES, bool MX>
 hipError_t pick(const NormArgs& a, hipStream_t s) {
-  const unsigned rows = (unsigned)a.rows;
-  if (a.cols <= 512)
-    rms_norm_kernel<64, 1, RES, MX><<<(rows + 3) / 4, 256, 0, s>>>(a);
-  else if (a.cols <= 1024)
-    rms_norm_kernel<64, 2, RES, MX><<<(rows + 3) / 4, 256, 0, s>>>(a);
-  else if (a.cols <= 2048)
-    rms_norm_kernel<256, 1, RES, MX><<<rows, 256, 0, s>>>(a);
-  else if (a.cols <= 4096)
-    rms_norm_kernel<512, 1, RES, MX><<<rows, 512, 0, s>>>(a);
-  else if (MX && a.cols <= 8192 && rows >= 256)
-    rms_norm_kernel<512, 2, RES, MX><<<rows, 512, 0, s>>>(a);
-  else if (a.cols <= 8192)
-    rms_norm_kernel<1024, 1, RES, MX><<<rows, 1024, 0, s>>>(a);
-  else if (a.cols <= 16384)
-    rms_norm_kernel<1024, 2, RES, MX><<<rows, 1024, 0, s>>>(a);
-  else
-    rms_norm_long_kernel<RES, MX><<<rows, 1024, 0, s>>>(a);
-  return hipGetLastError();
+  if (a.cols <= 512) return rows_of<64, 1, RES, MX>(a, s);
+  if (a.cols <= 1024) return rows_of<64, 2, RES, MX>(a, s);
+  if (a.cols <= 2048) return rows_of<256, 1, RES, MX>(a, s);
+  if (a.cols <= 4096) return rows_of<512, 1, RES, MX>(a, s);
+  if (MX && a.cols <= 8192 && a.rows >= 256) return rows_of<512, 2, RES, MX>(a, s);
+  if (a.cols <= 8192) return rows_of<1024, 1, RES, MX>(a, s);
+  if (a.cols <= 16384) return rows_of<1024, 2, RES, MX>(a, s);
+  return rows_of<1024, 0, RES, MX>(a, s);
 }
 
 }  // namespace
