@@ -95,34 +95,39 @@ __global__ __launch_bounds__(256) void kv_read_kernel(const KvArgs a) {
   *reinterpret_cast<u32x4*>(a.dst[w] + (p.token * a.heads + p.head) * D + p.piece * 8) = v;
 }
 
-unsigned blocks(const KvArgs& a) {
-  return (unsigned)((a.tokens * 2 * a.heads * (a.dim / 8) + 255) / 256);
+// A launch takes fewer than 2^32 threads: more tokens than that go in several
+// launches, of 2^31 threads at most.
+template <int D, bool Q8, bool WRITE>
+hipError_t run(const KvArgs& a, hipStream_t s) {
+  const int64_t per = (int64_t)2 * a.heads * (D / 8);   // threads of a token
+  const int64_t most = (int64_t(1) << 31) / per;
+  for (int64_t at = 0; at < a.tokens; at += most) {
+    KvArgs b = a;
+    b.tokens = a.tokens - at < most ? a.tokens - at : most;
+    b.slots += at;
+    for (int w = 0; w < 2; ++w) {
+      if (WRITE) b.src[w] += at * a.token_stride[w];
+      else b.dst[w] += at * a.heads * D;
+    }
+    const unsigned grid = (unsigned)((b.tokens * per + 255) / 256);
+    if (WRITE) kv_write_kernel<D, Q8><<<grid, 256, 0, s>>>(b);
+    else kv_read_kernel<D, Q8><<<grid, 256, 0, s>>>(b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <bool WRITE>
+hipError_t pick(const KvArgs& a, hipStream_t s) {
+  const bool q8 = a.scale[0] != nullptr;
+  if (a.dim == 64) return q8 ? run<64, true, WRITE>(a, s) : run<64, false, WRITE>(a, s);
+  return q8 ? run<128, true, WRITE>(a, s) : run<128, false, WRITE>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_kv_write(const KvArgs& a, hipStream_t s) {
-  const bool q8 = a.scale[0] != nullptr;
-  if (a.dim == 64) {
-    if (q8) kv_write_kernel<64, true><<<blocks(a), 256, 0, s>>>(a);
-    else kv_write_kernel<64, false><<<blocks(a), 256, 0, s>>>(a);
-  } else {
-    if (q8) kv_write_kernel<128, true><<<blocks(a), 256, 0, s>>>(a);
-    else kv_write_kernel<128, false><<<blocks(a), 256, 0, s>>>(a);
-  }
-  return hipGetLastError();
-}
-
-hipError_t launch_kv_read(const KvArgs& a, hipStream_t s) {
-  const bool q8 = a.scale[0] != nullptr;
-  if (a.dim == 64) {
-    if (q8) kv_read_kernel<64, true><<<blocks(a), 256, 0, s>>>(a);
-    else kv_read_kernel<64, false><<<blocks(a), 256, 0, s>>>(a);
-  } else {
-    if (q8) kv_read_kernel<128, true><<<blocks(a), 256, 0, s>>>(a);
-    else kv_read_kernel<128, false><<<blocks(a), 256, 0, s>>>(a);
-  }
-  return hipGetLastError();
-}
+hipError_t launch_kv_write(const KvArgs& a, hipStream_t s) { return pick<true>(a, s); }
+hipError_t launch_kv_read(const KvArgs& a, hipStream_t s) { return pick<false>(a, s); }
 
 }  // namespace bd

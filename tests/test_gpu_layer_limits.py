@@ -55,3 +55,33 @@ def test_rms_norm_of_more_rows_than_a_launch_takes(rows, cols, threads):
     few = T.rms_norm_mx(x[at], w, EPS, x[at])
     for got, want in zip(T.rms_norm_mx(x, w, EPS, x), few):
         assert torch.equal(got.view(torch.uint8)[at], want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_cache_calls_of_more_tokens_than_a_launch_takes(q8):
+    """Eight values a thread: 2 * tokens * heads * dim / 8 passes 2^32.  The rows
+    of neighbouring tokens overlap in memory, and all but a few of the tokens are
+    passed over."""
+    heads, dim, page, step = 1024, 128, 16, 8
+    part = 2 ** 31 // (2 * heads * dim // 8)
+    tokens = 2 * part + 5
+    at = _picked(tokens, part)
+    n = len(at)
+    kind = torch.float8_e4m3fn if q8 else torch.bfloat16
+    cache = [torch.zeros((1, heads, page, dim), dtype=kind, device=DEV) for _ in range(2)]
+    cache += [torch.zeros((1, heads, page), dtype=torch.uint8, device=DEV)
+              .view(torch.float8_e8m0fnu) for _ in range(2)] if q8 else [None, None]
+    k, v = (_randn((tokens * step + heads * dim,), i, 1.4)
+            .as_strided((tokens, heads, dim), (step, dim, 1)) for i in (4, 5))
+    slots = torch.full((tokens,), -1, dtype=torch.int32, device=DEV)
+    slots[at] = torch.arange(n, dtype=torch.int32, device=DEV)
+    T.kv_write(k, v, slots, *cache)
+    few = [None if c is None else torch.zeros_like(c) for c in cache]
+    T.kv_write(k[at], v[at], slots[at], *few)
+    for got, want in zip(cache, few):
+        if got is not None:
+            assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+    want = T.kv_read(slots[at], *cache)
+    for got, exp in zip(T.kv_read(slots, *cache), want):
+        assert torch.equal(got[at], exp)
+        assert bool(torch.isnan(got[at[1] + 1]).all())        # a slot outside the cache
