@@ -235,6 +235,7 @@ struct Join {
   Cut cut[2];
   float* partial[2];
   int items[2], from1;
+  int first;   // of this launch's workgroups
 };
 
 // A row's sums are held by D / 4 neighbouring lanes, four dims each; a
@@ -243,11 +244,11 @@ struct Join {
 // order of the additions is that of the plan, which the lengths alone decide.
 template <int D>
 __global__ __launch_bounds__(4 * D) void join_pieces_kernel(AttnArgs a, const Join j) {
-  const int which = (int)blockIdx.x >= j.from1;
+  const int at = j.first + (int)blockIdx.x, which = at >= j.from1;
   const Cut c = j.cut[which];
   a.partial = j.partial[which];
   a.items = j.items[which];
-  const int idx = (int)blockIdx.x - (which ? j.from1 : 0), per = c.R / 16;   // powers of two
+  const int idx = at - (which ? j.from1 : 0), per = c.R / 16;   // powers of two
   Item it;
   if (!find_item<true>(a, c, idx / per, it) || it.pieces == 1) return;
   // cu_q that does not rise could ask for more items than there are
@@ -424,7 +425,7 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
   __shared__ __attribute__((aligned(16))) char smem[SMEM];
 
   Item it;
-  if (!find_item<false>(a, c, blockIdx.x, it)) return;
+  if (!find_item<false>(a, c, a.first + (int)blockIdx.x, it)) return;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g4 = lane >> 4;
@@ -755,7 +756,7 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
   __shared__ __attribute__((aligned(16))) char smem[M::SMEM];
 
   Item it;
-  if (!find_item<false>(a, c, blockIdx.x, it)) return;
+  if (!find_item<false>(a, c, a.first + (int)blockIdx.x, it)) return;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rg = wv % RG, kg = wv / RG;
@@ -1220,6 +1221,19 @@ Way way_of(const AttnArgs& a) {
   return w;
 }
 
+// A launch takes fewer than 2^32 threads: more workgroups than that go in
+// several, of 2^31 threads each.
+template <typename F>
+hipError_t in_parts(int grid, int threads, F launch) {
+  const int most = (int)((int64_t(1) << 31) / threads);
+  for (int at = 0; at < grid; at += most) {
+    launch(at, (unsigned)(grid - at < most ? grid - at : most));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <int D, bool Q8>
 hipError_t run(AttnArgs a, hipStream_t s) {
   a.by_group = divisor(a.group);
@@ -1239,21 +1253,27 @@ hipError_t run(AttnArgs a, hipStream_t s) {
     AttnArgs b = a;
     b.items = w.items[k];
     b.partial = a.partial + (k ? w.bytes[0] / sizeof(float) : 0);
-    if (c.R == 16)
-      attend_rows16_kernel<D, Q8, NW, 2><<<b.items, NW * 64, 0, s>>>(b, c);
-    else if (c.R == 64)
-      attend_many_kernel<D, Q8, 2><<<b.items, 256, 0, s>>>(b, c);
-    else
-      attend_many_kernel<D, Q8, 4><<<b.items, 256, 0, s>>>(b, c);
+    const int threads = c.R == 16 ? NW * 64 : 256;
+    const hipError_t e = in_parts(b.items, threads, [&](int first, unsigned grid) {
+      b.first = first;
+      if (c.R == 16)
+        attend_rows16_kernel<D, Q8, NW, 2><<<grid, NW * 64, 0, s>>>(b, c);
+      else if (c.R == 64)
+        attend_many_kernel<D, Q8, 2><<<grid, 256, 0, s>>>(b, c);
+      else
+        attend_many_kernel<D, Q8, 4><<<grid, 256, 0, s>>>(b, c);
+    });
+    if (e != hipSuccess) return e;
     j.cut[k] = c;
     j.partial[k] = b.partial;
     j.items[k] = b.items;
     if (c.share != 0.f) joins[k] = (b.items - c.target - 8) * (c.R / 16);
   }
   j.from1 = joins[0];
-  if (joins[0] + joins[1] > 0)
-    join_pieces_kernel<D><<<(unsigned)(joins[0] + joins[1]), 4 * D, 0, s>>>(a, j);
-  return hipGetLastError();
+  return in_parts(joins[0] + joins[1], 4 * D, [&](int first, unsigned grid) {
+    j.first = first;
+    join_pieces_kernel<D><<<grid, 4 * D, 0, s>>>(a, j);
+  });
 }
 
 }  // namespace

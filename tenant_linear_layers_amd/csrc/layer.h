@@ -63,6 +63,7 @@ struct AttnArgs {
   Divisor by_group, by_page, by_heads;   // group, page, kv_heads (set by the launcher)
   int window;                // 0: none
   int items;                 // pieces that the workspace has room for (set by the launcher)
+  int first;                 // piece of a launch's first workgroup (set by the launcher)
   float scale_log2;          // softmax scale * log2(e)
 };
 size_t paged_attention_workspace(const AttnArgs& a);

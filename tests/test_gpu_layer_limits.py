@@ -85,3 +85,28 @@ def test_cache_calls_of_more_tokens_than_a_launch_takes(q8):
     for got, exp in zip(T.kv_read(slots, *cache), want):
         assert torch.equal(got[at], exp)
         assert bool(torch.isnan(got[at[1] + 1]).all())        # a slot outside the cache
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_attention_of_more_pieces_than_a_launch_takes(q8):
+    """A workgroup of 256 threads per sequence and head: more than 2^32 threads.
+    All sequences read the same few pages; lengths of one page are never cut."""
+    heads, dim, page = 1024, 64, 16
+    part = 2 ** 31 // 256 // heads
+    seqs = 2 * part + 5
+    pages = 7
+    kind = torch.float8_e4m3fn if q8 else torch.bfloat16
+    cache = [torch.zeros((pages, heads, page, dim), dtype=kind, device=DEV) for _ in range(2)]
+    cache += [torch.zeros((pages, heads, page), dtype=torch.uint8, device=DEV)
+              .view(torch.float8_e8m0fnu) for _ in range(2)] if q8 else [None, None]
+    rows = pages * page
+    T.kv_write(_randn((rows, heads, dim), 6), _randn((rows, heads, dim), 7),
+               torch.arange(rows, dtype=torch.int32, device=DEV), *cache)
+    at = _picked(seqs, part)
+    q = _randn((seqs, heads, dim), 8)
+    i = torch.arange(seqs, device=DEV, dtype=torch.int32)
+    table, kv = (i % pages).unsqueeze(1), 1 + i * 5 % page
+    cu = torch.arange(seqs + 1, device=DEV, dtype=torch.int32)
+    out = T.paged_attention(q, *cache[:2], table, cu, kv, 1, *cache[2:])
+    want = T.paged_attention(q[at], *cache[:2], table[at], cu[:len(at) + 1], kv[at], 1, *cache[2:])
+    assert torch.equal(out[at], want)
