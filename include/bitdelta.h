@@ -416,8 +416,9 @@ int bitdelta_monosoup_merge(const uint16_t* const* w_ft, int32_t k, const uint16
 /*
  * Decoder-layer operators beside the linears: the norm of the residual
  * stream, the paged key/value cache that the fused QKV rows go to, and
- * attention over it.  bf16 tensors here need the alignment of their elements
- * only (2 bytes); caches, 8-bit outputs and the workspace 16 bytes.  A call
+ * attention over it.  Caches with their scales, the norm's e4m3 output, the
+ * outputs of kv_read and paged_attention and the workspace need 16 bytes of
+ * alignment; other tensors that of their elements (2 bytes for bf16).  A call
  * of no rows or tokens returns BITDELTA_OK and enqueues nothing.
  *
  * Groups in 8 bits: e4m3 values (OCP, no infinities) with one power-of-two

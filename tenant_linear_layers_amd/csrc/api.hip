@@ -455,7 +455,7 @@ BD_EXPORT int bitdelta_kv_write(const uint16_t* k, const uint16_t* v, int64_t k_
   if (!k || !v || !slots || !k_cache || !v_cache || (k_scale != nullptr) != (v_scale != nullptr))
     return BITDELTA_ERR_NULL;
   if (!aligned2(k) || !aligned2(v) || !aligned4(slots) || !aligned16(k_cache) ||
-      !aligned16(v_cache))
+      !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
     return BITDELTA_ERR_ALIGN;
   const size_t rows = (size_t)pages * (size_t)page * (size_t)heads;
   const size_t cbytes = rows * (size_t)dim * (k_scale ? 1u : 2u);
@@ -505,7 +505,7 @@ BD_EXPORT int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t hea
   if (!k || !v || !slots || !k_cache || !v_cache || (k_scale != nullptr) != (v_scale != nullptr))
     return BITDELTA_ERR_NULL;
   if (!aligned16(k) || !aligned16(v) || !aligned4(slots) || !aligned16(k_cache) ||
-      !aligned16(v_cache))
+      !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
     return BITDELTA_ERR_ALIGN;
   const size_t rows = (size_t)pages * (size_t)page * (size_t)heads;
   const size_t cbytes = rows * (size_t)dim * (k_scale ? 1u : 2u);
