@@ -1,9 +1,9 @@
 """The decoder-layer operators on the GPU where their sizes meet a limit: calls
-of more threads than one launch takes, workspaces of exactly the size asked
-for, and calls that run beside each other.
+of more threads than one launch takes, and workspaces of exactly the size asked
+for.
 
-Comparisons are of bits: a row, or a sequence's plan, does not depend on what
-the test changes."""
+Where no tolerance is given bits are compared: what a row holds, or how a
+sequence is cut, does not depend on what the test changes."""
 
 import pytest
 import torch
@@ -110,3 +110,48 @@ def test_attention_of_more_pieces_than_a_launch_takes(q8):
     out = T.paged_attention(q, *cache[:2], table, cu, kv, 1, *cache[2:])
     want = T.paged_attention(q[at], *cache[:2], table[at], cu[:len(at) + 1], kv[at], 1, *cache[2:])
     assert torch.equal(out[at], want)
+
+
+# ------------------------------------------------------------------ workspaces
+def _serving(new, kv, heads, kv_heads, dim, page, q8, seed):
+    """The arguments of a call over a filled cache."""
+    need = [-(-m // page) for m in kv]
+    table = torch.full((len(kv), max(need)), -1, dtype=torch.int32)
+    order, at = torch.randperm(sum(need), generator=torch.Generator().manual_seed(seed)), 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    rows = sum(need) * page
+    shape = (sum(need), kv_heads, page, dim)
+    kind = torch.float8_e4m3fn if q8 else torch.bfloat16
+    cache = [torch.empty(shape, dtype=kind, device=DEV) for _ in range(2)]
+    cache += [torch.empty(shape[:3], dtype=torch.float8_e8m0fnu, device=DEV)
+              for _ in range(2)] if q8 else [None, None]
+    T.kv_write(_randn((rows, kv_heads, dim), seed, 1.4), _randn((rows, kv_heads, dim), seed + 1),
+               torch.arange(rows, dtype=torch.int32, device=DEV), *cache)
+    cu = torch.tensor([sum(new[:i]) for i in range(len(new) + 1)], dtype=torch.int32, device=DEV)
+    return dict(q=_randn((sum(new), heads, dim), seed + 2, 1.4), k_cache=cache[0],
+                v_cache=cache[1], table=table.to(DEV), cu_q=cu,
+                kv_len=torch.tensor(kv, dtype=torch.int32, device=DEV), max_q=max(new),
+                k_scale=cache[2], v_scale=cache[3])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("new,kv,heads,kv_heads,dim", [
+    ([1, 1, 1], [3000, 700, 5], 8, 2, 128),                  # few rows
+    ([1] * 90, [300 + 40 * i for i in range(90)], 4, 4, 64),
+    ([33], [4000], 8, 2, 128),                               # many rows, tiles of 64 and of 128
+    ([200], [5000], 8, 1, 64),
+    ([1, 90, 1, 3, 300, 17], [2500, 900, 40, 3000, 2048, 1000], 8, 2, 128),    # both in a call
+])
+def test_attention_keeps_to_a_workspace_of_the_size_asked_for(new, kv, heads, kv_heads, dim, q8):
+    p = _serving(new, kv, heads, kv_heads, dim, 16, q8, 11)
+    n = T.paged_attention_workspace_size(len(p["q"]), len(kv), p["max_q"], heads, kv_heads, dim,
+                                         p["table"].shape[1], 16)
+    assert n > 0
+    big = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device=DEV)
+    out = T.paged_attention(**p, workspace=big[4096:4096 + n])
+    assert torch.equal(out, T.paged_attention(**p))
+    assert bool((big[:4096] == 0xA5).all()) and bool((big[4096 + n:] == 0xA5).all())
+    with pytest.raises(T.BitDeltaError):
+        T.paged_attention(**p, workspace=big[4096:4096 + n - 16])
