@@ -1,9 +1,11 @@
 """The decoder-layer operators on the GPU where their sizes meet a limit: calls
-of more threads than one launch takes, and workspaces of exactly the size asked
-for.
+of more threads than one launch takes, workspaces of exactly the size asked
+for, tiles in about one round of the card, and calls that run beside each other.
 
 Where no tolerance is given bits are compared: what a row holds, or how a
 sequence is cut, does not depend on what the test changes."""
+
+import threading
 
 import pytest
 import torch
@@ -155,3 +157,101 @@ def test_attention_keeps_to_a_workspace_of_the_size_asked_for(new, kv, heads, kv
     assert bool((big[:4096] == 0xA5).all()) and bool((big[4096 + n:] == 0xA5).all())
     with pytest.raises(T.BitDeltaError):
         T.paged_attention(**p, workspace=big[4096:4096 + n - 16])
+
+
+# ------------------------------------------------------------------ tiles of many rows
+def _definition(p):
+    """(out, sum of probability times |v|) in float64, a sequence and head at a
+    time, from the values that the cache holds."""
+    q, heads, dim = p["q"].double(), p["q"].shape[1], p["q"].shape[2]
+    _, kv_heads, page, _ = p["k_cache"].shape
+    out, mag = torch.zeros_like(q), torch.zeros_like(q)
+    for b, m in enumerate(p["kv_len"].tolist()):
+        first, last = p["cu_q"][b:b + 2].tolist()
+        j = torch.arange(m, device=DEV)
+        slots = (p["table"][b][j // page] * page + j % page).int()
+        k, v = (x.double() for x in T.kv_read(slots, p["k_cache"], p["v_cache"], p["k_scale"],
+                                              p["v_scale"]))
+        i = torch.arange(m - (last - first), m, device=DEV).unsqueeze(1)
+        for h in range(heads):
+            kk, vv = (x[:, h * kv_heads // heads].contiguous() for x in (k, v))
+            z = (q[first:last, h].contiguous() @ kk.t().contiguous()) / dim ** 0.5
+            w = torch.softmax(z.masked_fill(j > i, float("-inf")), 1)
+            out[first:last, h] = w @ vv
+            mag[first:last, h] = w @ vv.abs()
+    return out, mag
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("new,kv,heads,kv_heads,dim", [
+    ([1600], [1600], 16, 2, 128),        # tiles of 64 rows, cut: 200 tiles of 128, half a round
+    ([1000], [2100], 32, 8, 64),         # the same where the new tokens are just half of the keys
+    ([700, 900], [700, 900], 16, 2, 64),
+    ([2048], [2048], 32, 4, 128),        # tiles of 64 rows, not cut: two rounds of them
+    ([2048], [2048], 32, 4, 64),
+    ([2048], [2048], 64, 8, 64),         # tiles of 128 rows, not cut
+    ([2011], [2011], 64, 8, 128),        # and a little short of that
+])
+def test_attention_of_rounds_of_tiles(new, kv, heads, kv_heads, dim, q8):
+    """Tolerance: probabilities rounded to bf16 (2^-8 of each), scores and sums in
+    float32 (below 2^-13 of the probabilities), the output rounded to bf16."""
+    p = _serving(new, kv, heads, kv_heads, dim, 16, q8, 21)
+    ref, mag = _definition(p)
+    bad = (T.paged_attention(**p).double() - ref).abs() > \
+        2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -12) * mag
+    assert not bool(bad.any()), f"{int(bad.sum())} values off"
+
+
+# ------------------------------------------------------------------ calls beside each other
+def _layer_calls(seed, q8):
+    """What a layer does between its linears, as a function of a stream."""
+    p = _serving([1, 40, 3], [700, 400, 2000], 8, 2, 128, 16, q8, seed)
+    x, r = _randn((44, 1024), seed + 3, 1.4), _randn((44, 1024), seed + 4, 3.0)
+    w = _randn((1024,), seed + 5, 0.1) + 1.0
+    k, v = _randn((44, 2, 128), seed + 6), _randn((44, 2, 128), seed + 7)
+    cache = [c if c is None else torch.zeros_like(c[:4])
+             for c in (p["k_cache"], p["v_cache"], p["k_scale"], p["v_scale"])]
+    slots = torch.randperm(64, generator=torch.Generator().manual_seed(seed))[:44].int().to(DEV)
+
+    def run(stream=None):
+        y, h = T.rms_norm(x, w, EPS, r, stream=stream)
+        q, s, _ = T.rms_norm_mx(x, w, EPS, r, stream=stream)
+        T.kv_write(k, v, slots, *cache, stream=stream)
+        back = T.kv_read(slots, *cache, stream=stream)
+        o = T.paged_attention(**p, stream=stream)
+        return [t.view(torch.uint8) for t in (y, h, q, s, *back, o)]
+
+    return run
+
+
+def test_calls_on_two_streams_at_once():
+    runs = [_layer_calls(31, False), _layer_calls(51, True)]
+    want = [run() for run in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    got = [[run(s) for run, s in zip(runs, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for one in got:
+        for a, b in zip(one, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_calls_from_several_threads_at_once():
+    runs = [_layer_calls(71 + 20 * i, i % 2 == 1) for i in range(4)]
+    want = [run() for run in runs]
+    torch.cuda.synchronize()
+    got = [None] * len(runs)
+
+    def work(i):
+        s = torch.cuda.Stream()
+        got[i] = [runs[i](s) for _ in range(5)]
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(runs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for many, b in zip(got, want):
+        for a in many:
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
