@@ -425,7 +425,11 @@ int bitdelta_monosoup_merge(const uint16_t* const* w_ft, int32_t k, const uint16
  * scale in e8m0 (a byte e + 127).  The scale is the smallest 2^e with
  * max|x| <= 448 * 2^e, e kept within -120..120 (-120 for a group of zeros);
  * magnitudes above 240 * 2^120 (infinities among them) are held to it, NaN
- * becomes e4m3's NaN and has no part in the scale.
+ * becomes e4m3's NaN and has no part in the scale.  (This is not the rule of the
+ * OCP MX text, whose scale is taken of the maximum's logarithm rounded down, and
+ * under which values next to the maximum may saturate.)  In a cache filled by
+ * other means every byte is read as e8m0 says, but that attention may count byte
+ * 0 as zero and byte 255, e8m0's NaN, as an infinity.
  *
  * bitdelta_rms_norm - h = x + residual; y = h / sqrt(mean(h^2) + eps) * w.
  * Sums are float32, taken of the unrounded h (a row whose sum of squares
@@ -494,7 +498,7 @@ int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_
  *             bounds is read.  kv_len is held to width * page.
  *   cu_q      device, int32 [seqs + 1], rising; held to [0, tokens].  Rows of
  *             out that no sequence has are not written.
- *   max_q     the largest n; rows past it may not be computed
+ *   max_q     the largest n, or more; a sequence of more rows may be left out
  *   scale     above 0 and finite, as is its product with log2(e)
  *   out       device, bf16 [tokens, heads, dim], contiguous, written
  *   workspace device, >= bitdelta_paged_attention_workspace_size(...) bytes

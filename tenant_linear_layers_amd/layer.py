@@ -151,7 +151,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual=None, y
 def rms_norm_mx(x: torch.Tensor, weight: torch.Tensor, eps: float, residual=None, h=None,
                 stream=None):
     """(q, scale, h): rms_norm with its output in e4m3 [..., cols] and one
-    e8m0 scale per 32 values [..., cols / 32]."""
+    e8m0 scale per 32 values [..., cols / 32]: the smallest power of two under
+    which none of them passes 448, so that no value saturates (the OCP MX text
+    takes the maximum's logarithm rounded down)."""
     return _norm(x, weight, eps, residual, None, h, stream, True)
 
 
@@ -285,7 +287,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     q: bf16 [tokens, heads, dim], any token and head strides; table: int32
     [seqs, width] page ids; cu_q: int32 [seqs + 1], the sequences' rows of q;
     kv_len: int32 [seqs], cached keys of each, the new tokens' among them;
-    max_q: the most rows of a sequence; window: keys a row sees, 0 for all;
+    max_q: the most rows of a sequence, or more (a sequence of more than max_q
+    may be left out); window: keys a row sees, 0 for all;
     scale: of the scores, above 0, 1 / sqrt(dim) by default.  A row that sees no key
     gives zeros."""
     dev = _device(q, "q")
