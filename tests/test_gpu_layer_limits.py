@@ -255,3 +255,29 @@ def test_calls_from_several_threads_at_once():
     for many, b in zip(got, want):
         for a in many:
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ------------------------------------------------------------------ weights
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("new,kv,heads,kv_heads,dim", [
+    ([1] * 20, [100 + 37 * i for i in range(20)], 8, 2, 128),      # few rows
+    ([1, 1, 2], [4000, 1500, 90], 8, 4, 64),                       # cut into pieces
+    ([40, 70], [300, 900], 8, 2, 128),                             # many rows
+    ([200], [1000], 8, 1, 64),
+])
+def test_attention_over_one_value_gives_that_value(new, kv, heads, kv_heads, dim, q8):
+    """The weights, as the product with V takes them, add up to one: float32's
+    roundings are far below half a step of the result, which is next to a power of
+    two, where the steps are smallest.  Scores of some tens, so that of most rows
+    one key has most of the weight, and seldom a weight of one."""
+    p = _serving(new, kv, heads, kv_heads, dim, 16, q8, 91)
+    p["q"] = (p["q"].float() * 8).to(torch.bfloat16)
+    value = 1.875 if q8 else 1.9921875
+    rows = p["v_cache"].shape[0] * 16
+    T.kv_write(_randn((rows, kv_heads, dim), 91, 1.4),
+               torch.full((rows, kv_heads, dim), value, dtype=torch.bfloat16, device=DEV),
+               torch.arange(rows, dtype=torch.int32, device=DEV), p["k_cache"], p["v_cache"],
+               p["k_scale"], p["v_scale"])
+    out = T.paged_attention(**p)
+    off = out != value
+    assert not bool(off.any()), f"{int(off.sum())} of {off.numel()} values off"
