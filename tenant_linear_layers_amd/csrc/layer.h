@@ -59,11 +59,11 @@ struct AttnArgs {
   float* partial;            // workspace
   int64_t q_token_stride, q_head_stride;
   int64_t pages;
+  int first;                 // piece of a launch's first workgroup (set by the launcher)
   int tokens, seqs, max_q, heads, kv_heads, group, dim, page, width;
   Divisor by_group, by_page, by_heads;   // group, page, kv_heads (set by the launcher)
   int window;                // 0: none
   int items;                 // pieces that the workspace has room for (set by the launcher)
-  int first;                 // piece of a launch's first workgroup (set by the launcher)
   float scale_log2;          // softmax scale * log2(e)
 };
 size_t paged_attention_workspace(const AttnArgs& a);
