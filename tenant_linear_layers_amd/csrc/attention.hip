@@ -1193,15 +1193,32 @@ int64_t most_items(const AttnArgs& a, const Cut& c) {
 // where
 // * the average sequence would leave 128 too empty (40 tokens, 160 rows: 31.4
 //   us against 33.4; of 64 dims 25.9 against 30.6), or
-// * the tiles of 128 are about one round of the card and their lengths differ,
-//   new tokens being about half or more of the keys: 2048 tokens of 32 heads 61 us
-//   against 66, of 64 dims 37 against 47 (of 64 heads, two rounds, 118 against
-//   92; 512 tokens, a quarter of a round, 29 against 24).
+// * the tiles of 128 are about one round of the card, 512, and their lengths
+//   differ, new tokens being about half or more of the keys: a long tile is then
+//   what the call waits for.  The more tiles there are, the longer the sequences
+//   have to be for that, and half as much again for 64 dims, whose steps are
+//   shorter against what a workgroup starts and ends with (us with tiles of 64 /
+//   of 128; 8 bits in brackets):
+//     280 tokens of 64 heads, 136 tiles   22.6 / 23.3   (fewer than 200: 340, 168
+//                                                       tiles, 24.5 / 22.8)
+//     512 of 64 heads, 256 tiles          26.1 / 32.9   (28.2 / 34.4)
+//     840 of 64 heads, 416                44.1 / 36.7   (48.8 / 39.0)
+//     2048 of 32 heads, 512               61.8 / 66.3   (68.7 / 70.5)
+//     2400 of 32 heads, 600               81.8 / 79.0   (90.5 / 83.8)
+//     4800 of 16 heads, 600               129.9 / 136.5 (144.2 / 144.7)
+//     4 sequences of 200, 64 heads, 400   36.3 / 24.4   (40.4 / 25.5)
+//     64 dims: 840 of 64 heads, 416       28.7 / 25.8   (31.9 / 29.6)
+//              1680 of 32 heads, 416      31.3 / 39.1   (40.9 / 45.1)
+//              1200 of 64 heads, 600      33.6 / 34.1   (42.3 / 38.2)
+//   Over 1.25 times as many cached keys 64 rows are slower where sequences are
+//   long (1680 tokens of 16 heads 69 / 69, in 8 bits 77 / 73; of 32 heads 125 /
+//   111), not where they are short (420 of 64 heads 31 / 38).
 int rows_a_tile(const AttnArgs& a) {
   const int64_t all = (int64_t)a.tokens * a.group, each = all / a.seqs;
   const bool filled = (each + 127) / 128 * 128 * 4 <= (each + 63) / 64 * 64 * 5;
   const int64_t tiles = all / 128 * a.kv_heads;
-  const bool uneven = tiles >= 200 && tiles < 1000 &&
+  const int64_t most = 200 + a.max_q / (a.dim == 64 ? 4 : 6);
+  const bool uneven = tiles >= 200 && tiles < (most < 1000 ? most : 1000) &&
                       (int64_t)a.max_q * 9 >= (int64_t)a.width * a.page * 4;
   return filled && !uneven ? 128 : 64;
 }
