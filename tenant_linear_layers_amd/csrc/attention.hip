@@ -1199,17 +1199,19 @@ int64_t most_items(const AttnArgs& a, const Cut& c) {
 //   have to be for that, and half as much again for 64 dims, whose steps are
 //   shorter against what a workgroup starts and ends with (us with tiles of 64 /
 //   of 128; 8 bits in brackets):
-//     280 tokens of 64 heads, 136 tiles   22.6 / 23.3   (fewer than 200: 340, 168
-//                                                       tiles, 24.5 / 22.8)
-//     512 of 64 heads, 256 tiles          26.1 / 32.9   (28.2 / 34.4)
-//     840 of 64 heads, 416                44.1 / 36.7   (48.8 / 39.0)
-//     2048 of 32 heads, 512               61.8 / 66.3   (68.7 / 70.5)
-//     2400 of 32 heads, 600               81.8 / 79.0   (90.5 / 83.8)
-//     4800 of 16 heads, 600               129.9 / 136.5 (144.2 / 144.7)
-//     4 sequences of 200, 64 heads, 400   36.3 / 24.4   (40.4 / 25.5)
-//     64 dims: 840 of 64 heads, 416       28.7 / 25.8   (31.9 / 29.6)
-//              1680 of 32 heads, 416      31.3 / 39.1   (40.9 / 45.1)
-//              1200 of 64 heads, 600      33.6 / 34.1   (42.3 / 38.2)
+//     280 tokens of 64 heads, 136 tiles   21.8 / 21.4   (fewer than 200: 24.0 / 22.4)
+//     512 of 64 heads, 256 tiles          20.6 / 32.5   (22.9 / 34.3)
+//     800 of 64 heads, 400                36.8 / 36.3   (40.6 / 39.1)
+//     1200 of 64 heads, 600               59.6 / 42.7   (65.6 / 44.4)
+//     1200 of 32 heads, 296               30.8 / 42.8   (35.1 / 44.8)
+//     1600 of 32 heads, 400               47.0 / 53.5   (51.5 / 56.7)
+//     2400 of 32 heads, 600               83.1 / 71.5   (91.6 / 75.6)
+//     4800 of 16 heads, 600               131.2 / 129.0 (144.4 / 136.3)
+//     4 sequences of 200, 64 heads, 400   37.1 / 25.1   (40.9 / 26.4)
+//     64 dims: 800 of 64 heads, 400       21.0 / 26.0   (27.3 / 29.7)
+//              1200 of 64 heads, 600      34.2 / 29.6   (42.8 / 33.5)
+//              2048 of 32 heads, 512      39.4 / 42.5   (45.6 / 48.5)
+//              4800 of 16 heads, 600      80.7 / 89.7   (92.8 / 101.4)
 //   Over 1.25 times as many cached keys 64 rows are slower where sequences are
 //   long (1680 tokens of 16 heads 69 / 69, in 8 bits 77 / 73; of 32 heads 125 /
 //   111), not where they are short (420 of 64 heads 31 / 38).
@@ -1241,11 +1243,15 @@ Way way_of(const AttnArgs& a) {
     Cut& c = w.cut[k];
     if (!c.R) continue;
     // cut only where a tile can be longer than the shortest piece, and, for
-    // many rows, where the tiles by themselves are not two rounds of the card
-    // (2048 tokens of 64 heads: 92 us, cut 107).  Pieces of 8 blocks or more:
-    // of 16 / 32, 24 mixed sequences take 36 / 40 us for 32.
+    // many rows, where the tiles by themselves are not a round of the card, 512:
+    // a cut call has its join (5 us and more) and its pieces' sums to set against
+    // shorter ends.  64 heads, whole / cut: 1060 tokens, 528 tiles, 38.1 / 46.4
+    // us, 1060 over 4240 cached 251 / 259, 2000 tokens 83 / 97, 2048 86 / 100; 420
+    // over 1680, 208 tiles, 55 / 55, over 6720 175 / 134.  (From nothing whole
+    // tiles are faster below a round too: 840 tokens, 416 tiles, 32 / 39.)  Pieces
+    // of 8 blocks or more: of 16 / 32, 24 mixed sequences take 36 / 40 us for 32.
     const bool may = ((int64_t)a.width * a.page + 31) / 32 + 1 > c.min_blocks &&
-                     (k == 0 || (int64_t)a.tokens * a.group / c.R * a.kv_heads < 2 * c.target);
+                     (k == 0 || (int64_t)a.tokens * a.group / c.R * a.kv_heads < c.target);
     c.share = may ? (float)a.kv_heads / (float)c.round : 0.f;
     AttnArgs b = a;
     if (k == 0 && rows > 16) b.max_q = 16 / a.group;
