@@ -1242,16 +1242,24 @@ Way way_of(const AttnArgs& a) {
   for (int k = 0; k < 2; ++k) {
     Cut& c = w.cut[k];
     if (!c.R) continue;
-    // cut only where a tile can be longer than the shortest piece, and, for
-    // many rows, where the tiles by themselves are not a round of the card, 512:
-    // a cut call has its join (5 us and more) and its pieces' sums to set against
+    // Cut only where a tile can be longer than the shortest piece, and, for many
+    // rows, where the tiles by themselves are not a round of the card, 512: a cut
+    // call has its join (5 us and more) and its pieces' sums to set against
     // shorter ends.  64 heads, whole / cut: 1060 tokens, 528 tiles, 38.1 / 46.4
     // us, 1060 over 4240 cached 251 / 259, 2000 tokens 83 / 97, 2048 86 / 100; 420
     // over 1680, 208 tiles, 55 / 55, over 6720 175 / 134.  (From nothing whole
-    // tiles are faster below a round too: 840 tokens, 416 tiles, 32 / 39.)  Pieces
-    // of 8 blocks or more: of 16 / 32, 24 mixed sequences take 36 / 40 us for 32.
-    const bool may = ((int64_t)a.width * a.page + 31) / 32 + 1 > c.min_blocks &&
-                     (k == 0 || (int64_t)a.tokens * a.group / c.R * a.kv_heads < c.target);
+    // tiles are faster below a round too: 840 tokens, 416 tiles, 32 / 39.)
+    // Sequences whose cached keys may be many times their new ones can be of very
+    // different lengths, and are cut up to two rounds: 8 sequences of 128 tokens
+    // over 0 to 12000 keys, 512 tiles, 207 / 113; of 128 tokens and no more 24 / 25,
+    // of 300 to 600 tokens, 880 tiles, 50 / 64.
+    // Pieces of 8 blocks or more: of 16, 16 tokens of 64 heads over 1500 keys take
+    // 23 us for 19, over 8000 29 for 31, 512 from nothing, of 32 heads, 21 for 24.
+    const int64_t keys = (int64_t)a.width * a.page;
+    const bool alike = a.seqs == 1 || keys <= 4 * (int64_t)a.max_q;
+    const bool may = (keys + 31) / 32 + 1 > c.min_blocks &&
+                     (k == 0 || (int64_t)a.tokens * a.group / c.R * a.kv_heads <
+                                    (alike ? c.target : 2 * c.target));
     c.share = may ? (float)a.kv_heads / (float)c.round : 0.f;
     AttnArgs b = a;
     if (k == 0 && rows > 16) b.max_q = 16 / a.group;
