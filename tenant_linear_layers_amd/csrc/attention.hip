@@ -31,8 +31,6 @@
 namespace bd {
 namespace {
 
-typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
-typedef u32x4 u32x4_any __attribute__((aligned(2)));  // strided rows of any alignment
 typedef short s16x4 __attribute__((__vector_size__(8)));
 typedef int i32x2 __attribute__((__vector_size__(8)));
 #define BD_LDS __attribute__((address_space(3)))

@@ -15,12 +15,6 @@
 namespace bd {
 namespace {
 
-typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
-typedef u32x4 u32x4_any __attribute__((aligned(2)));  // strided rows of any alignment
-
-__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-
 // One lane's place: which cache (0 k, 1 v), token, head and the eight values.
 struct Place {
   int which, head, piece;

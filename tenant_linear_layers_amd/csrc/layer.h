@@ -5,7 +5,18 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "common.h"
+
 namespace bd {
+
+typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
+// 16 bytes at an address aligned to its 2-byte elements only (rows of an odd
+// length, strided rows): one load or store of the full width all the same.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+// The two bf16 values of a dword.
+__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
 // y = h / sqrt(mean(h^2) + eps) * w of each row, h = x + residual.  scale !=
 // nullptr: y is e4m3 with one e8m0 scale per 32 values.

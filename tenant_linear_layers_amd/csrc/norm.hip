@@ -16,19 +16,12 @@
 namespace bd {
 namespace {
 
-// 16 bytes at an address aligned to its 2-byte elements only (rows of an odd
-// length, strided rows): one load or store of the full width all the same.
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
-
 __device__ __forceinline__ u32x4 ld8(const uint16_t* p) {
   return *reinterpret_cast<const u32x4_any*>(p);
 }
 __device__ __forceinline__ void st8(uint16_t* p, u32x4 v) {
   *reinterpret_cast<u32x4_any*>(p) = v;
 }
-
-__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
 // Up to eight elements from p, zeros past n.
 __device__ __forceinline__ u32x4 ld_some(const uint16_t* p, int n) {
@@ -138,7 +131,6 @@ __device__ __forceinline__ void put(const NormArgs& a, int64_t row, int col, int
   m = fmaxf(m, __shfl_xor(m, 2));
   const uint32_t sb = scale_byte(m);
   const float is = inv_scale(sb);
-  typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
   const u32x2 o = {pack_e4m3(y[0] * is, y[1] * is, y[2] * is, y[3] * is),
                    pack_e4m3(y[4] * is, y[5] * is, y[6] * is, y[7] * is)};
   *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.y) + row * a.cols + col) = o;
