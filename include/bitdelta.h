@@ -490,7 +490,7 @@ int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_
  * Query head h reads key/value head h / (heads / kv_heads).  A row that sees
  * no key is zero.  NaN and infinities in the cache or in q reach the rows that
  * see them only.  Scores, maxima and sums are float32; the probabilities
- * are rounded to bf16 for the product with v.
+ * are rounded to bf16 for the product with v, and add up to one as rounded.
  *   q         device, bf16 [tokens, heads, dim], strides in elements
  *   table     device, int32 [seqs, width]; entries of pages that no row sees
  *             are not read.  A page outside [0, pages) that a row sees makes

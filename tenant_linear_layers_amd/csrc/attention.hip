@@ -157,7 +157,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Cut& c, int i
                         (float)c.min_blocks);
   const float per_C = 1.f / C;
   // A rest of half a piece or less is none of its own: 32 sequences in bf16
-  // 151 us, with it 163 (64 in 8 bits 143 / 142; 24 mixed ones 32.5 / 33.9).
+  // 152 us, with it 163 (64 in 8 bits 144 / 142; 24 mixed ones 30.7 / 30.4).
   auto pieces_of = [&](int blocks) {
     return max((int)fmaf((float)(blocks - 1), per_C, -0.5f) + 1, 1);
   };
@@ -345,7 +345,10 @@ __device__ __forceinline__ void query_range(const AttnArgs& a, const Tile& t, in
 // what is left of the rounding is the mean of 2^-9 (v_j - o) over the keys, so
 // rows of one value give that value (over 16 keys whose heaviest stands 2^5.3
 // above the reference an error of 0.0013 of the output, 0.0025 against the total
-// before rounding; over 16000 keys 0.0020 and 0.0021).
+// before rounding; over 16000 keys 0.0020 and 0.0021).  A second product with
+// what the rounding leaves off would take that error away: for few rows it costs
+// 0 to 3.5% (a token at 4097 keys 14.3 / 14.8 us, 40 sequences of 8000 233 / 237),
+// for many it is half as many matrix products again.
 __device__ __forceinline__ uint32_t weights(float p0, float p1, float& l) {
   const uint32_t two = cvt_pk_bf16(p0, p1);
   l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two),
@@ -420,10 +423,10 @@ __device__ __forceinline__ void wait_lds() {
 // coalesced; only the pieces of a row are permuted) and are read back as
 // matrix operands, so there is no barrier until the waves' sums are joined.
 //
-// Bound by HBM: 64 sequences in 8 bits (688 MB) take 134 us, 5.1 TB/s, 32 in
+// Bound by HBM: 64 sequences in 8 bits (688 MB) take 137 us, 5.0 TB/s, 32 in
 // bf16 (795 MB) 142 us, 5.6 TB/s (a copy reaches 4.9 on this card); the CUs
 // stand idle a fifth of the time at the ends.  A single token at 4097 keys,
-// 10.4 us, is a chain of latencies: plan, page table, K, V, joins.
+// 10.1 us, is a chain of latencies: plan, page table, K, V, joins.
 template <int D, bool Q8, int NW, int U>
 __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a, const Cut c) {
   constexpr int R = 16;
@@ -737,12 +740,14 @@ __global__ __launch_bounds__(NW * 64) void attend_rows16_kernel(const AttnArgs a
 // so that the matrix cores work while rows are staged and maxima taken: K is
 // wanted one step before V, and their two rings in LDS are NB steps deep each.
 //
-// A prompt of 2048 (64 heads of 128) takes 90 us, 760 TFLOP/s, a chunk of 509
-// over 16384 keys in 8 bits 306 us, 907 TFLOP/s; the matrix cores are busy 33%
-// and 40% of the time (rocprofv3).  What bounds it is the latency of a wave's
-// step: one workgroup a CU takes twice the time, and no part left out (the
-// exponentials, the reads of K or V, the barrier) saves more than 5%.  The
-// registers (64 sums, 32 of Q, 32 scores a lane) allow two waves a SIMD.
+// A prompt of 2048 (64 heads of 128) takes 84 us, 820 TFLOP/s, a chunk of 509
+// over 16384 keys in 8 bits 297 us with its join, 934 TFLOP/s; the matrix cores
+// are busy 34% and 41% of the time (rocprofv3).  What bounds bf16 is the latency
+// of a wave's step: one workgroup a CU takes twice the time, and of its parts,
+// left out one at a time, the staging gives 14%, the exponentials, the reads of K
+// or V, the look or the barrier 5% at most.  In 8 bits the staging is the largest
+// part: without its loads, conversions and writes to LDS a step is 23% shorter.
+// The registers (64 sums, 32 of Q, 32 scores a lane) allow two waves a SIMD.
 //
 // bf16 rows go straight from memory to LDS.  e4m3 rows pass through registers
 // and are written as bf16, each times its scale (exact), so that the
@@ -879,8 +884,8 @@ __global__ __launch_bounds__(256, 2) void attend_many_kernel(const AttnArgs a, c
       const u32x4 got = raw[slot][w][j];
       // A lane has two neighbouring pieces of 16 bytes.  Every other four lanes
       // write theirs in opposite order, so that eight lanes write to all banks:
-      // half of the conflicts, a chunk of 509 over 16384 keys 326 / 330 us.  For
-      // 64 dims the exchange costs more (16000 tokens 1477 / 1455 us).
+      // half of the conflicts, a chunk of 509 over 16384 keys 296 / 300 us.  For
+      // 64 dims the exchange costs more (16000 tokens of 16 heads 635 / 623 us).
       const bool swap = D == 128 && (lane & 4);
       const u32x4 r = {swap ? got[2] : got[0], swap ? got[3] : got[1], swap ? got[0] : got[2],
                        swap ? got[1] : got[3]};
@@ -1191,10 +1196,10 @@ int64_t most_items(const AttnArgs& a, const Cut& c) {
 
 // Rows of a tile of many rows.  128 rows read half of what tiles of 64 read
 // and need not share a workgroup's keys out: 200 tokens over 8000 keys, 4 rows
-// a token, 53 us against 78 (8 bits, 128 dims; of 64 dims 44 against 55).  64
+// a token, 54 us against 77 (8 bits, 128 dims; of 64 dims 41 against 53).  64
 // where
-// * the average sequence would leave 128 too empty (40 tokens, 160 rows: 31.4
-//   us against 33.4; of 64 dims 25.9 against 30.6), or
+// * the average sequence would leave 128 too empty (40 tokens, 160 rows, over
+//   8000 keys: 30.5 us against 33.0; of 64 dims 24.9 against 29.1), or
 // * the tiles of 128 are about one round of the card, 512, and their lengths
 //   differ, new tokens being about half or more of the keys: a long tile is then
 //   what the call waits for.  The more tiles there are, the longer the sequences
@@ -1232,9 +1237,9 @@ Way way_of(const AttnArgs& a) {
   const int64_t rows = (int64_t)a.max_q * a.group;
   const int kAll = 2147483647;
   // 128 pieces of little work, not one a CU: their join is longer than what the
-  // other CUs would save (a token at 4097 keys 15.2 / 15.9 us, in 8 bits 14.1 /
-  // 15.0).  1024 of more: 32 sequences in bf16 151 us, 1280 158 us, 1536 154; 40
-  // sequences of 8000 keys 231, 242 and 254.
+  // other CUs would save (a token at 4097 keys 14.2 / 14.8 us, in 8 bits 13.7 /
+  // 14.5).  1024 of more: 32 sequences in bf16 152 us, 1280 158 us, 1536 155; 40
+  // sequences of 8000 keys 231, 245 and 255 (64 in 8 bits 144, 141 and 141).
   w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 128, 1024, 4, 16, 0, 16, 0.f};
   if (rows > 16) {
     w.cut[1] = Cut{rows_a_tile(a), 512, 512, 8, 64, 0, kAll, 0.f};
@@ -1292,8 +1297,8 @@ hipError_t run(AttnArgs a, hipStream_t s) {
   const Way w = way_of(a);
   // Waves of a workgroup of few rows: two rings of 64 KB at most fit a CU, and
   // then the second workgroup's start and end lie under the first one's loads.
-  // bf16 rows of 128 dims with 2 / 4 waves: a token at 4097 keys 15.9 / 19.6
-  // us, 4 of them 22.7 / 28.1, 32 sequences of up to 16000 keys 163 / 160.
+  // bf16 rows of 128 dims with 2 / 4 waves: a token at 4097 keys 14.2 / 13.9
+  // us, 4 of them 22.7 / 27.4, 32 sequences of up to 16000 keys 152 / 156.
   constexpr int NW = !Q8 && D == 128 ? 2 : 4;
   Join j{};
   int joins[2] = {0, 0};
