@@ -24,7 +24,7 @@ def _gpu():
         pytest.skip("no GPU")
     T.lib()
     yield
-    torch.cuda.empty_cache()          # these tests hold up to 70 GB
+    torch.cuda.empty_cache()          # these tests hold up to 90 GB
 
 
 def _randn(shape, seed, std=1.0):
