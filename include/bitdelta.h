@@ -414,12 +414,13 @@ int bitdelta_monosoup_merge(const uint16_t* const* w_ft, int32_t k, const uint16
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Decoder-layer operators beside the linears: the norm of the residual
- * stream, the paged key/value cache that the fused QKV rows go to, and
- * attention over it.  Caches with their scales, the norm's e4m3 output, the
- * outputs of kv_read and paged_attention and the workspace need 16 bytes of
- * alignment; other tensors that of their elements (2 bytes for bf16).  A call
- * of no rows or tokens returns BITDELTA_OK and enqueues nothing.
+ * Decoder-layer operators beside the linears: the norms of the residual
+ * stream, rotary positions, the paged key/value cache that the fused QKV rows
+ * go to, and attention over it.  Caches with their scales, the norm's e4m3
+ * output, the outputs of kv_read and paged_attention and the workspace need 16
+ * bytes of alignment; other tensors that of their elements (2 bytes for bf16),
+ * a table that rotary_table writes 8.  A call of no rows or tokens returns
+ * BITDELTA_OK and enqueues nothing.
  *
  * Groups in 8 bits: e4m3 values (OCP, no infinities) with one power-of-two
  * scale in e8m0 (a byte e + 127).  The scale is the smallest 2^e with
@@ -452,12 +453,73 @@ int bitdelta_rms_norm_mx(const uint16_t* x, int64_t x_stride, const uint16_t* re
                          int64_t cols, uint16_t* h_out, uint8_t* y, uint8_t* scale, void* stream);
 
 /*
- * Paged cache: k_cache and v_cache are [pages, heads, page, dim], bf16 or
- * e4m3; the 8-bit form has k_scale and v_scale, e8m0 [pages, heads, page], one
- * per row (a token's dim values of one head).  The scales are NULL for bf16.
+ * bitdelta_rms_norm_block - the norm after a block, the block's gate and
+ * residual, and the norm before the next block, in one pass:
+ *   u = x / sqrt(mean(x^2) + eps) * post    (post NULL: u = x)
+ *   h = residual + alpha * gate * u         (gate NULL: 1)
+ *   y = h / sqrt(mean(h^2) + eps) * w
+ * Everything between the inputs and the roundings of h_out and y to bf16 is
+ * float32; the second norm is taken of the unrounded h.
+ *   x, residual, gate   device, bf16 [rows, cols], rows x_stride / r_stride /
+ *                       g_stride elements apart (0: one row for all)
+ *   post, w             device, bf16 [cols]
+ *   alpha               finite
+ *   h_out, y            device, bf16 [rows, cols], written
+ * rows below 2^31, cols 1..2^30, rows * cols below 2^40.
+ */
+int bitdelta_rms_norm_block(const uint16_t* x, int64_t x_stride, const uint16_t* post,
+                            const uint16_t* gate, int64_t g_stride, float alpha,
+                            const uint16_t* residual, int64_t r_stride, const uint16_t* w,
+                            float eps, int64_t rows, int64_t cols, uint16_t* h_out, uint16_t* y,
+                            void* stream);
+
+/*
+ * Rotary positions.  A table is float32 [length, rot / 2, 2]: cosine and sine
+ * of each position's angle for each pair of dims.
+ *
+ * bitdelta_rotary_table writes the positions first .. first + length - 1 of
+ * one: magnitude * cos and sin of position * frequencies[pair], taken in 64
+ * bits and rounded once.  frequencies: device, float64 [pairs]; pairs
+ * 1..32768; first and length below 2^31.
+ *
+ * bitdelta_rotary turns the first rot dims (even, 2..dim) of each head by the
+ * angle of its token's position,
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * where (a, b) are the dims (i, i + rot / 2), or (2 i, 2 i + 1) with
+ * interleaved != 0; the dims behind them are copied.  Products and their sum
+ * are rounded to float32 one by one, the result to bf16.
+ *   x, out     device, bf16 [tokens, heads, dim], tokens and heads the given
+ *              strides (in elements) apart, the dims contiguous.  out's rows
+ *              lie apart (BITDELTA_ERR_SHAPE otherwise); it may be x, of the
+ *              same strides, and overlaps no input in another way
+ *   positions  device, int32 [tokens]; one outside [0, length) makes the
+ *              turned dims NaN
+ * heads 1..65536, dim 2..65536, length below 2^31, length * rot below 2^40.
+ */
+int bitdelta_rotary_table(const double* frequencies, int64_t pairs, int64_t first, int64_t length,
+                          double magnitude, float* table, void* stream);
+int bitdelta_rotary(const uint16_t* x, int64_t x_token_stride, int64_t x_head_stride,
+                    const int32_t* positions, const float* table, int64_t length, int64_t rot,
+                    int32_t interleaved, int64_t tokens, int64_t heads, int64_t dim,
+                    uint16_t* out, int64_t out_token_stride, int64_t out_head_stride,
+                    void* stream);
+
+/*
+ * Paged cache: k_cache and v_cache are [pages, heads, page, dim], bf16, e4m3
+ * or, in the _4bit calls, e2m1 (two values a byte, the even dim low); the 8-bit
+ * form has k_scale and v_scale, e8m0 [pages, heads, page], one per row (a
+ * token's dim values of one head), the 4-bit form e8m0 [pages, heads, page,
+ * dim / 32], one per 32 dims.  The scales are NULL for bf16.
  * Slot s is row s % page of page s / page.  dim is 64 or 128, page a multiple
  * of 16 up to 65536, heads 1..1024, pages * page below 2^31
  * and, times heads, at most 2^35.
+ *
+ * Groups in 4 bits: e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives)
+ * with the scale that is the smallest 2^e with max|x| <= 6 * 2^e, e kept
+ * within -120..120 (-120 for a group of zeros); magnitudes above 6 * 2^120
+ * (infinities among them) are held to it.  e2m1 has no NaN: a group that holds
+ * one gets the scale byte 255, e8m0's NaN, and all of it is NaN.  In a cache
+ * filled by other means every byte is read as e8m0 says.
  *
  * bitdelta_kv_write puts row t of k and v into slot slots[t]; a slot outside
  * the cache (a negative one for padding) is passed over.  The slots of a call
@@ -478,6 +540,39 @@ int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_
                      int64_t pages, int64_t page, const void* k_cache, const void* v_cache,
                      const uint8_t* k_scale, const uint8_t* v_scale, uint16_t* k, uint16_t* v,
                      void* stream);
+int bitdelta_kv_write_4bit(const uint16_t* k, const uint16_t* v, int64_t k_token_stride,
+                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                           const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim,
+                           int64_t pages, int64_t page, void* k_cache, void* v_cache,
+                           uint8_t* k_scale, uint8_t* v_scale, void* stream);
+int bitdelta_kv_read_4bit(const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim,
+                          int64_t pages, int64_t page, const void* k_cache, const void* v_cache,
+                          const uint8_t* k_scale, const uint8_t* v_scale, uint16_t* k,
+                          uint16_t* v, void* stream);
+
+/*
+ * bitdelta_kv_append - what a step has between its QKV product and its
+ * attention, in one pass: q turned as bitdelta_rotary does, to q_out, and the
+ * rows of a bitdelta_kv_write of k, turned alike, and v.  k goes from the
+ * rotation's float32 to the cache's type with one rounding.  bits is that of
+ * the cache: 16, 8 or 4, with scales as above.
+ *   q          device, bf16 [tokens, heads, dim] with strides, heads 1..1024
+ *   k, v       device, bf16 [tokens, kv_heads, dim] with strides
+ *   positions, table, length, rot, interleaved   as in bitdelta_rotary; the
+ *              same for q and k
+ *   slots      as in bitdelta_kv_write; the q of a token whose slot is outside
+ *              the cache is turned all the same
+ *   q_out      device, bf16 [tokens, heads, dim], contiguous, written; it
+ *              overlaps no input
+ */
+int bitdelta_kv_append(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                       const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride,
+                       const uint16_t* v, int64_t v_token_stride, int64_t v_head_stride,
+                       const int32_t* positions, const float* table, int64_t length, int64_t rot,
+                       int32_t interleaved, const int32_t* slots, int64_t tokens, int64_t heads,
+                       int64_t kv_heads, int64_t dim, int64_t pages, int64_t page, int32_t bits,
+                       void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                       uint16_t* q_out, void* stream);
 
 /*
  * bitdelta_paged_attention - causal attention of new tokens over the cache.
@@ -518,6 +613,16 @@ int bitdelta_paged_attention(const uint16_t* q, int64_t q_token_stride, int64_t 
                              int64_t page, int64_t width, float scale, int64_t window,
                              uint16_t* out, void* workspace, size_t workspace_bytes,
                              void* stream);
+
+/* bitdelta_paged_attention_4bit - the same over a 4-bit cache, its scales
+ * [pages, kv_heads, page, dim / 32]; the same workspace. */
+int bitdelta_paged_attention_4bit(
+    const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+    const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* table,
+    const int32_t* cu_q, const int32_t* kv_len, int64_t tokens, int64_t seqs, int64_t max_q,
+    int64_t heads, int64_t kv_heads, int64_t dim, int64_t pages, int64_t page, int64_t width,
+    float scale, int64_t window, uint16_t* out, void* workspace, size_t workspace_bytes,
+    void* stream);
 
 /*
  * Calibration probes - measured ceilings for the rooflines of the kernels

@@ -105,3 +105,63 @@ def paged_attention(q, k, v, table, cu_q, kv_len, window=0, scale=None):
                 out[cu_q[b] + i, h] = w @ vv
                 mag[cu_q[b] + i, h] = w @ np.abs(vv)
     return out, mag
+
+
+# ------------------------------------------------------------------ 4 bits
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+GROUP4 = 32
+HOLD4 = 6.0 * 2.0 ** 120
+NAN_SCALE = 255
+
+
+def e2m1_codes(x: np.ndarray) -> np.ndarray:
+    """Nearest e2m1 code of values up to 6 in magnitude, ties to the even code."""
+    a = np.abs(x)
+    i = np.clip(np.searchsorted(E2M1, a, side="right") - 1, 0, 7)
+    j = np.minimum(i + 1, 7)
+    lo, hi = a - E2M1[i], E2M1[j] - a
+    up = (hi < lo) | ((hi == lo) & (i % 2 == 1) & (j > i))
+    return (np.where(up, j, i) | np.where(np.signbit(x), 8, 0)).astype(np.uint8)
+
+
+def quantise4(x: np.ndarray):
+    """(bytes [..., dim / 2], scale bytes [..., dim / 32]) of rows [..., dim]: a
+    group with a NaN is NaN, its codes zero."""
+    g = x.reshape(*x.shape[:-1], -1, GROUP4)
+    nan = np.isnan(g).any(-1)
+    g = np.where(nan[..., None], 0.0, np.clip(g, -HOLD4, HOLD4))
+    amax = np.abs(g).max(-1)
+    e = np.full(amax.shape, -120, np.int64)
+    for _ in range(240):
+        e += (e < 120) & (amax > 6.0 * np.exp2(e.astype(np.float64)))
+    c = np.where(nan[..., None], 0, e2m1_codes(g / np.exp2(e.astype(np.float64))[..., None]))
+    c = c.reshape(x.shape).astype(np.uint8)
+    return c[..., 0::2] | (c[..., 1::2] << 4), np.where(nan, NAN_SCALE, e + 127).astype(np.uint8)
+
+
+def dequantise4(q: np.ndarray, scale: np.ndarray) -> np.ndarray:
+    """float64 rows of bytes and scale bytes, as e8m0 says (255: NaN)."""
+    c = np.stack([q & 15, q >> 4], -1).reshape(*q.shape[:-1], -1)
+    v = np.where(c & 8, -1.0, 1.0) * E2M1[c & 7]
+    s = np.where(scale == NAN_SCALE, np.nan, np.exp2(scale.astype(np.float64) - 127.0))
+    return v * np.repeat(s, GROUP4, axis=-1)
+
+
+# ------------------------------------------------------------------ rotary positions
+def rotary(x, angles, interleaved=False):
+    """x [tokens, heads, dim] turned by angles [tokens, rot / 2], as complex numbers."""
+    half = angles.shape[1]
+    out = np.array(x, np.float64)
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else \
+        (slice(0, half), slice(half, 2 * half))
+    z = (out[..., a] + 1j * out[..., b]) * np.exp(1j * angles)[:, None, :]
+    out[..., a], out[..., b] = z.real, z.imag
+    return out
+
+
+# ------------------------------------------------------------------ around a block
+def rms_norm_block(x, residual, post, weight, eps, gate=None, scale=1.0):
+    """(y, h) in float64."""
+    u = x if post is None else rms_norm(x, post, eps)[0]
+    h = residual + scale * (1.0 if gate is None else gate) * u
+    return rms_norm(h, weight, eps)[0], h

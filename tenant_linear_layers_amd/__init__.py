@@ -40,10 +40,15 @@ from .bitdelta import (  # noqa: F401
 )
 from .deltafile import delta_blob, load_delta, read_delta_header, save_delta  # noqa: F401
 from .layer import (  # noqa: F401
+    kv_append,
     kv_read,
     kv_write,
     paged_attention,
     paged_attention_workspace_size,
     rms_norm,
+    rms_norm_block,
     rms_norm_mx,
+    rotary,
+    rotary_frequencies,
+    rotary_table,
 )

@@ -68,8 +68,15 @@ EXPORTS = (
     "bitdelta_rms_norm_mx",
     "bitdelta_kv_write",
     "bitdelta_kv_read",
+    "bitdelta_kv_write_4bit",
+    "bitdelta_kv_read_4bit",
+    "bitdelta_kv_append",
+    "bitdelta_rms_norm_block",
+    "bitdelta_rotary_table",
+    "bitdelta_rotary",
     "bitdelta_paged_attention_workspace_size",
     "bitdelta_paged_attention",
+    "bitdelta_paged_attention_4bit",
     "bitdelta_probe_stream_read",
     "bitdelta_probe_mfma_bf16",
     "bitdelta_probe_decode_loads",
@@ -164,11 +171,28 @@ def lib() -> ctypes.CDLL:
     L.bitdelta_kv_write.restype = i32
     L.bitdelta_kv_read.argtypes = [vp] + [i64] * 5 + [vp] * 7
     L.bitdelta_kv_read.restype = i32
+    L.bitdelta_kv_write_4bit.argtypes = L.bitdelta_kv_write.argtypes
+    L.bitdelta_kv_write_4bit.restype = i32
+    L.bitdelta_kv_read_4bit.argtypes = L.bitdelta_kv_read.argtypes
+    L.bitdelta_kv_read_4bit.restype = i32
+    L.bitdelta_kv_append.argtypes = ([vp, i64, i64] * 3 + [vp, vp, i64, i64, ctypes.c_int32, vp] +
+                                     [i64] * 6 + [ctypes.c_int32] + [vp] * 6)
+    L.bitdelta_kv_append.restype = i32
+    L.bitdelta_rms_norm_block.argtypes = [vp, i64, vp, vp, i64, f32, vp, i64, vp, f32, i64, i64,
+                                          vp, vp, vp]
+    L.bitdelta_rms_norm_block.restype = i32
+    L.bitdelta_rotary_table.argtypes = [vp, i64, i64, i64, ctypes.c_double, vp, vp]
+    L.bitdelta_rotary_table.restype = i32
+    L.bitdelta_rotary.argtypes = ([vp, i64, i64, vp, vp, i64, i64, ctypes.c_int32] + [i64] * 3 +
+                                  [vp, i64, i64, vp])
+    L.bitdelta_rotary.restype = i32
     L.bitdelta_paged_attention_workspace_size.argtypes = [i64] * 8
     L.bitdelta_paged_attention_workspace_size.restype = sz
     L.bitdelta_paged_attention.argtypes = ([vp, i64, i64] + [vp] * 7 + [i64] * 9 + [f32, i64] +
                                            [vp, vp, sz, vp])
     L.bitdelta_paged_attention.restype = i32
+    L.bitdelta_paged_attention_4bit.argtypes = L.bitdelta_paged_attention.argtypes
+    L.bitdelta_paged_attention_4bit.restype = i32
     L.bitdelta_probe_stream_read.argtypes = [vp, sz, ctypes.c_int32, vp, vp]
     L.bitdelta_probe_stream_read.restype = i32
     L.bitdelta_probe_mfma_bf16.argtypes = [ctypes.c_int32, ctypes.c_int32, vp, vp]

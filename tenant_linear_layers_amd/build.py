@@ -22,7 +22,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbitdelta.so")
 
 SOURCES = ("api.hip", "compress.hip", "decode.hip", "prefill.hip", "reconstruct.hip",
-           "cache.hip", "monosoup.hip", "probe.hip", "norm.hip", "kvcache.hip", "attention.hip")
+           "cache.hip", "monosoup.hip", "probe.hip", "norm.hip", "rotary.hip", "kvcache.hip",
+           "attention.hip", "attention4.hip")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -439,32 +439,48 @@ BD_EXPORT int bitdelta_rms_norm_mx(const uint16_t* x, int64_t x_stride, const ui
                   stream);
 }
 
-BD_EXPORT int bitdelta_kv_write(const uint16_t* k, const uint16_t* v, int64_t k_token_stride,
-                                int64_t k_head_stride, int64_t v_token_stride,
-                                int64_t v_head_stride, const int32_t* slots, int64_t tokens,
-                                int64_t heads, int64_t dim, int64_t pages, int64_t page,
-                                void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
-                                void* stream) {
-  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+namespace {
+
+// Bytes of a cache's rows, and of their scales, in bf16, e4m3 or e2m1.
+size_t cache_bytes(size_t rows, int64_t dim, int bits) {
+  return rows * (size_t)dim * (size_t)bits / 8u;
+}
+size_t scale_bytes(size_t rows, int64_t dim, int bits) {
+  return bits == 4 ? rows * (size_t)(dim / 32) : rows;
+}
+// Scales are there as the format wants them: for 8 bits as k_scale says.
+bool scales_ok(const uint8_t* k_scale, const uint8_t* v_scale, int bits) {
+  return (k_scale != nullptr) == (bits != 16) && (v_scale != nullptr) == (bits != 16);
+}
+
+bool strides_ok(int64_t a, int64_t b) {
+  return a >= 0 && b >= 0 && a < kMaxElems && b < kMaxElems;
+}
+
+// Everything of a call that puts rows into a cache, its inputs' checks but for
+// those of an append's.
+int kv_write_args(const uint16_t* k, const uint16_t* v, const int64_t (&strides)[4],
+                  const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim, int64_t pages,
+                  int64_t page, int bits, void* k_cache, void* v_cache, uint8_t* k_scale,
+                  uint8_t* v_scale, bd::KvArgs& a) {
   if (!cache_shape_ok(heads, dim, pages, page) || tokens < 0 || tokens > kInt32Max ||
       tokens * heads * dim >= kMaxElems)
     return BITDELTA_ERR_SHAPE;
-  for (int64_t s : strides)
-    if (s < 0 || s >= kMaxElems) return BITDELTA_ERR_SHAPE;
+  if (!strides_ok(strides[0], strides[1]) || !strides_ok(strides[2], strides[3]))
+    return BITDELTA_ERR_SHAPE;
   if (tokens == 0) return BITDELTA_OK;
-  if (!k || !v || !slots || !k_cache || !v_cache || (k_scale != nullptr) != (v_scale != nullptr))
+  if (!k || !v || !slots || !k_cache || !v_cache || !scales_ok(k_scale, v_scale, bits))
     return BITDELTA_ERR_NULL;
   if (!aligned2(k) || !aligned2(v) || !aligned4(slots) || !aligned16(k_cache) ||
       !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
     return BITDELTA_ERR_ALIGN;
   const size_t rows = (size_t)pages * (size_t)page * (size_t)heads;
-  const size_t cbytes = rows * (size_t)dim * (k_scale ? 1u : 2u);
+  const size_t cbytes = cache_bytes(rows, dim, bits), sbytes = scale_bytes(rows, dim, bits);
   const void* outs[4] = {k_cache, v_cache, k_scale, v_scale};
-  const size_t outn[4] = {cbytes, cbytes, rows, rows};
+  const size_t outn[4] = {cbytes, cbytes, sbytes, sbytes};
   const void* ins[3] = {k, v, slots};
-  const size_t inn[3] = {span(tokens, k_token_stride, heads, k_head_stride, dim),
-                         span(tokens, v_token_stride, heads, v_head_stride, dim),
-                         (size_t)tokens * 4u};
+  const size_t inn[3] = {span(tokens, strides[0], heads, strides[1], dim),
+                         span(tokens, strides[2], heads, strides[3], dim), (size_t)tokens * 4u};
   for (int i = 0; i < 4; ++i) {
     if (!outs[i]) continue;
     for (int j = 0; j < 3; ++j)
@@ -472,9 +488,6 @@ BD_EXPORT int bitdelta_kv_write(const uint16_t* k, const uint16_t* v, int64_t k_
     for (int j = i + 1; j < 4; ++j)
       if (outs[j] && overlap(outs[i], outn[i], outs[j], outn[j])) return BITDELTA_ERR_OVERLAP;
   }
-  const int dev = check_device();
-  if (dev != BITDELTA_OK) return dev;
-  bd::KvArgs a{};
   a.src[0] = k;
   a.src[1] = v;
   a.cache[0] = k_cache;
@@ -482,36 +495,50 @@ BD_EXPORT int bitdelta_kv_write(const uint16_t* k, const uint16_t* v, int64_t k_
   a.scale[0] = k_scale;
   a.scale[1] = v_scale;
   a.slots = slots;
-  a.token_stride[0] = k_token_stride;
-  a.token_stride[1] = v_token_stride;
-  a.head_stride[0] = k_head_stride;
-  a.head_stride[1] = v_head_stride;
+  a.token_stride[0] = strides[0];
+  a.token_stride[1] = strides[2];
+  a.head_stride[0] = strides[1];
+  a.head_stride[1] = strides[3];
   a.tokens = tokens;
   a.n_slots = pages * page;
   a.heads = (int)heads;
   a.dim = (int)dim;
   a.page = (int)page;
+  a.bits = bits;
+  return BITDELTA_OK;
+}
+
+int kv_write(const uint16_t* k, const uint16_t* v, const int64_t (&strides)[4],
+             const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim, int64_t pages,
+             int64_t page, int bits, void* k_cache, void* v_cache, uint8_t* k_scale,
+             uint8_t* v_scale, void* stream) {
+  bd::KvArgs a{};
+  const int st = kv_write_args(k, v, strides, slots, tokens, heads, dim, pages, page, bits,
+                               k_cache, v_cache, k_scale, v_scale, a);
+  if (st != BITDELTA_OK || tokens == 0) return st;
+  const int dev = check_device();
+  if (dev != BITDELTA_OK) return dev;
   return status_of(bd::launch_kv_write(a, static_cast<hipStream_t>(stream)));
 }
 
-BD_EXPORT int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim,
-                               int64_t pages, int64_t page, const void* k_cache,
-                               const void* v_cache, const uint8_t* k_scale,
-                               const uint8_t* v_scale, uint16_t* k, uint16_t* v, void* stream) {
+int kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim, int64_t pages,
+            int64_t page, int bits, const void* k_cache, const void* v_cache,
+            const uint8_t* k_scale, const uint8_t* v_scale, uint16_t* k, uint16_t* v,
+            void* stream) {
   if (!cache_shape_ok(heads, dim, pages, page) || tokens < 0 || tokens > kInt32Max ||
       tokens * heads * dim >= kMaxElems)
     return BITDELTA_ERR_SHAPE;
   if (tokens == 0) return BITDELTA_OK;
-  if (!k || !v || !slots || !k_cache || !v_cache || (k_scale != nullptr) != (v_scale != nullptr))
+  if (!k || !v || !slots || !k_cache || !v_cache || !scales_ok(k_scale, v_scale, bits))
     return BITDELTA_ERR_NULL;
   if (!aligned16(k) || !aligned16(v) || !aligned4(slots) || !aligned16(k_cache) ||
       !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
     return BITDELTA_ERR_ALIGN;
   const size_t rows = (size_t)pages * (size_t)page * (size_t)heads;
-  const size_t cbytes = rows * (size_t)dim * (k_scale ? 1u : 2u);
+  const size_t cbytes = cache_bytes(rows, dim, bits), sbytes = scale_bytes(rows, dim, bits);
   const size_t obytes = (size_t)(tokens * heads * dim) * 2u;
   const void* ins[5] = {k_cache, v_cache, k_scale, v_scale, slots};
-  const size_t inn[5] = {cbytes, cbytes, rows, rows, (size_t)tokens * 4u};
+  const size_t inn[5] = {cbytes, cbytes, sbytes, sbytes, (size_t)tokens * 4u};
   for (int j = 0; j < 5; ++j)
     if (ins[j] && (overlap(k, obytes, ins[j], inn[j]) || overlap(v, obytes, ins[j], inn[j])))
       return BITDELTA_ERR_OVERLAP;
@@ -531,7 +558,219 @@ BD_EXPORT int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t hea
   a.heads = (int)heads;
   a.dim = (int)dim;
   a.page = (int)page;
+  a.bits = bits;
   return status_of(bd::launch_kv_read(a, static_cast<hipStream_t>(stream)));
+}
+
+bool table_shape_ok(int64_t length, int64_t rot, int64_t dim) {
+  return length >= 1 && length <= kInt32Max && rot >= 2 && rot % 2 == 0 && rot <= dim &&
+         length * rot < kMaxElems;
+}
+
+}  // namespace
+
+BD_EXPORT int bitdelta_rms_norm_block(const uint16_t* x, int64_t x_stride, const uint16_t* post,
+                                      const uint16_t* gate, int64_t g_stride, float alpha,
+                                      const uint16_t* residual, int64_t r_stride,
+                                      const uint16_t* w, float eps, int64_t rows, int64_t cols,
+                                      uint16_t* h_out, uint16_t* y, void* stream) {
+  if (rows < 0 || rows > kInt32Max || cols < 1 || cols > kMaxDin || rows * cols >= kMaxElems ||
+      !std::isfinite(alpha))
+    return BITDELTA_ERR_SHAPE;
+  if (rows == 0) return BITDELTA_OK;
+  if (!x || !residual || !w || !h_out || !y) return BITDELTA_ERR_NULL;
+  if (!strides_ok(x_stride, r_stride) || (gate && !strides_ok(g_stride, 0)))
+    return BITDELTA_ERR_SHAPE;
+  if (!aligned2(x) || !aligned2(post) || !aligned2(gate) || !aligned2(residual) || !aligned2(w) ||
+      !aligned2(h_out) || !aligned2(y))
+    return BITDELTA_ERR_ALIGN;
+  const size_t n = (size_t)rows * (size_t)cols * 2u, one = (size_t)cols * 2u;
+  const void* outs[2] = {y, h_out};
+  const void* ins[5] = {x, residual, gate, post, w};
+  const size_t inn[5] = {span(rows, x_stride, 1, 0, cols), span(rows, r_stride, 1, 0, cols),
+                         span(rows, g_stride, 1, 0, cols), one, one};
+  for (const void* o : outs)
+    for (int j = 0; j < 5; ++j)
+      if (ins[j] && overlap(o, n, ins[j], inn[j])) return BITDELTA_ERR_OVERLAP;
+  if (overlap(y, n, h_out, n)) return BITDELTA_ERR_OVERLAP;
+  const int dev = check_device();
+  if (dev != BITDELTA_OK) return dev;
+  bd::BlockNormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.gate = gate;
+  a.post = post;
+  a.w = w;
+  a.h = h_out;
+  a.y = y;
+  a.x_stride = x_stride;
+  a.r_stride = r_stride;
+  a.g_stride = g_stride;
+  a.rows = rows;
+  a.cols = (int)cols;
+  a.alpha = alpha;
+  a.eps = eps;
+  return status_of(bd::launch_rms_norm_block(a, static_cast<hipStream_t>(stream)));
+}
+
+BD_EXPORT int bitdelta_rotary_table(const double* frequencies, int64_t pairs, int64_t first,
+                                    int64_t length, double magnitude, float* table, void* stream) {
+  if (pairs < 1 || pairs > 32768 || first < 0 || first > kInt32Max || length < 0 ||
+      length > kInt32Max || length * pairs * 2 >= kMaxElems)
+    return BITDELTA_ERR_SHAPE;
+  if (length == 0) return BITDELTA_OK;
+  if (!frequencies || !table) return BITDELTA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(frequencies) & 7u) || (reinterpret_cast<uintptr_t>(table) & 7u))
+    return BITDELTA_ERR_ALIGN;
+  if (overlap(table, (size_t)(length * pairs) * 8u, frequencies, (size_t)pairs * 8u))
+    return BITDELTA_ERR_OVERLAP;
+  const int dev = check_device();
+  if (dev != BITDELTA_OK) return dev;
+  return status_of(bd::launch_rotary_table(frequencies, (int)pairs, first, length, magnitude,
+                                           table, static_cast<hipStream_t>(stream)));
+}
+
+BD_EXPORT int bitdelta_rotary(const uint16_t* x, int64_t x_token_stride, int64_t x_head_stride,
+                              const int32_t* positions, const float* table, int64_t length,
+                              int64_t rot, int32_t interleaved, int64_t tokens, int64_t heads,
+                              int64_t dim, uint16_t* out, int64_t out_token_stride,
+                              int64_t out_head_stride, void* stream) {
+  if (tokens < 0 || tokens > kInt32Max || heads < 1 || heads > 65536 || dim < 2 || dim > 65536 ||
+      tokens * heads * dim >= kMaxElems || !table_shape_ok(length, rot, dim) ||
+      !strides_ok(x_token_stride, x_head_stride) ||
+      !strides_ok(out_token_stride, out_head_stride))
+    return BITDELTA_ERR_SHAPE;
+  // rows of out lie apart, tokens outside of heads or the other way round
+  const int64_t ts = out_token_stride, hs = out_head_stride;
+  if (!((hs >= dim || heads == 1) && (ts >= (heads - 1) * hs + dim || tokens <= 1)) &&
+      !((ts >= dim || tokens <= 1) && (hs >= (tokens - 1) * ts + dim || heads == 1)))
+    return BITDELTA_ERR_SHAPE;
+  if (tokens == 0) return BITDELTA_OK;
+  if (!x || !positions || !table || !out) return BITDELTA_ERR_NULL;
+  if (!aligned2(x) || !aligned2(out) || !aligned4(positions) || !aligned4(table))
+    return BITDELTA_ERR_ALIGN;
+  const size_t on = span(tokens, ts, heads, hs, dim);
+  const bool same = x == out && (tokens == 1 || x_token_stride == ts) &&
+                    (heads == 1 || x_head_stride == hs);
+  if ((!same && overlap(out, on, x, span(tokens, x_token_stride, heads, x_head_stride, dim))) ||
+      overlap(out, on, positions, (size_t)tokens * 4u) ||
+      overlap(out, on, table, (size_t)(length * rot) * 4u))
+    return BITDELTA_ERR_OVERLAP;
+  const int dev = check_device();
+  if (dev != BITDELTA_OK) return dev;
+  bd::RotaryArgs a{};
+  a.x = x;
+  a.out = out;
+  a.positions = positions;
+  a.table = table;
+  a.x_token_stride = x_token_stride;
+  a.x_head_stride = x_head_stride;
+  a.out_token_stride = ts;
+  a.out_head_stride = hs;
+  a.tokens = tokens;
+  a.length = (int)length;
+  a.heads = (int)heads;
+  a.dim = (int)dim;
+  a.rot = (int)rot;
+  a.interleaved = interleaved != 0;
+  return status_of(bd::launch_rotary(a, static_cast<hipStream_t>(stream)));
+}
+
+BD_EXPORT int bitdelta_kv_append(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                 const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride,
+                                 const uint16_t* v, int64_t v_token_stride, int64_t v_head_stride,
+                                 const int32_t* positions, const float* table, int64_t length,
+                                 int64_t rot, int32_t interleaved, const int32_t* slots,
+                                 int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
+                                 int64_t pages, int64_t page, int32_t bits, void* k_cache,
+                                 void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                                 uint16_t* q_out, void* stream) {
+  if ((bits != 16 && bits != 8 && bits != 4) || heads < 1 || heads > 1024 ||
+      !strides_ok(q_token_stride, q_head_stride) || !table_shape_ok(length, rot, dim))
+    return BITDELTA_ERR_SHAPE;
+  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  bd::KvArgs a{};
+  const int st = kv_write_args(k, v, strides, slots, tokens, kv_heads, dim, pages, page, bits,
+                               k_cache, v_cache, k_scale, v_scale, a);
+  if (st != BITDELTA_OK) return st;
+  if (tokens * heads * dim >= kMaxElems) return BITDELTA_ERR_SHAPE;
+  if (tokens == 0) return BITDELTA_OK;
+  if (!q || !positions || !table || !q_out) return BITDELTA_ERR_NULL;
+  if (!aligned2(q) || !aligned4(positions) || !aligned4(table) || !aligned2(q_out))
+    return BITDELTA_ERR_ALIGN;
+  const size_t rows = (size_t)pages * (size_t)page * (size_t)kv_heads;
+  const size_t cbytes = cache_bytes(rows, dim, bits), sbytes = scale_bytes(rows, dim, bits);
+  const void* outs[5] = {q_out, k_cache, v_cache, k_scale, v_scale};
+  const size_t outn[5] = {(size_t)(tokens * heads * dim) * 2u, cbytes, cbytes, sbytes, sbytes};
+  const void* ins[6] = {q, positions, table, k, v, slots};
+  const size_t inn[6] = {span(tokens, q_token_stride, heads, q_head_stride, dim),
+                         (size_t)tokens * 4u, (size_t)(length * rot) * 4u,
+                         span(tokens, k_token_stride, kv_heads, k_head_stride, dim),
+                         span(tokens, v_token_stride, kv_heads, v_head_stride, dim),
+                         (size_t)tokens * 4u};
+  for (int i = 0; i < 5; ++i) {
+    if (!outs[i]) continue;
+    for (int j = 0; j < 6; ++j)
+      if (overlap(outs[i], outn[i], ins[j], inn[j])) return BITDELTA_ERR_OVERLAP;
+    if (i > 0 && overlap(q_out, outn[0], outs[i], outn[i])) return BITDELTA_ERR_OVERLAP;
+  }
+  const int dev = check_device();
+  if (dev != BITDELTA_OK) return dev;
+  bd::RotaryArgs r{};
+  r.x = q;
+  r.out = q_out;
+  r.positions = positions;
+  r.table = table;
+  r.x_token_stride = q_token_stride;
+  r.x_head_stride = q_head_stride;
+  r.out_token_stride = heads * dim;
+  r.out_head_stride = dim;
+  r.tokens = tokens;
+  r.length = (int)length;
+  r.heads = (int)heads;
+  r.dim = (int)dim;
+  r.rot = (int)rot;
+  r.interleaved = interleaved != 0;
+  return status_of(bd::launch_kv_append(a, r, static_cast<hipStream_t>(stream)));
+}
+
+BD_EXPORT int bitdelta_kv_write(const uint16_t* k, const uint16_t* v, int64_t k_token_stride,
+                                int64_t k_head_stride, int64_t v_token_stride,
+                                int64_t v_head_stride, const int32_t* slots, int64_t tokens,
+                                int64_t heads, int64_t dim, int64_t pages, int64_t page,
+                                void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                                void* stream) {
+  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  return kv_write(k, v, strides, slots, tokens, heads, dim, pages, page, k_scale ? 8 : 16, k_cache,
+                  v_cache, k_scale, v_scale, stream);
+}
+
+BD_EXPORT int bitdelta_kv_write_4bit(const uint16_t* k, const uint16_t* v, int64_t k_token_stride,
+                                     int64_t k_head_stride, int64_t v_token_stride,
+                                     int64_t v_head_stride, const int32_t* slots, int64_t tokens,
+                                     int64_t heads, int64_t dim, int64_t pages, int64_t page,
+                                     void* k_cache, void* v_cache, uint8_t* k_scale,
+                                     uint8_t* v_scale, void* stream) {
+  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  return kv_write(k, v, strides, slots, tokens, heads, dim, pages, page, 4, k_cache, v_cache,
+                  k_scale, v_scale, stream);
+}
+
+BD_EXPORT int bitdelta_kv_read(const int32_t* slots, int64_t tokens, int64_t heads, int64_t dim,
+                               int64_t pages, int64_t page, const void* k_cache,
+                               const void* v_cache, const uint8_t* k_scale,
+                               const uint8_t* v_scale, uint16_t* k, uint16_t* v, void* stream) {
+  return kv_read(slots, tokens, heads, dim, pages, page, k_scale ? 8 : 16, k_cache, v_cache,
+                 k_scale, v_scale, k, v, stream);
+}
+
+BD_EXPORT int bitdelta_kv_read_4bit(const int32_t* slots, int64_t tokens, int64_t heads,
+                                    int64_t dim, int64_t pages, int64_t page, const void* k_cache,
+                                    const void* v_cache, const uint8_t* k_scale,
+                                    const uint8_t* v_scale, uint16_t* k, uint16_t* v,
+                                    void* stream) {
+  return kv_read(slots, tokens, heads, dim, pages, page, 4, k_cache, v_cache, k_scale, v_scale, k,
+                 v, stream);
 }
 
 namespace {
@@ -571,8 +810,10 @@ BD_EXPORT size_t bitdelta_paged_attention_workspace_size(int64_t tokens, int64_t
       attention_sizes(tokens, seqs, max_q, heads, kv_heads, dim, width, page));
 }
 
-BD_EXPORT int bitdelta_paged_attention(
-    const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+namespace {
+
+int paged_attention(
+    int bits, const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
     const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* table,
     const int32_t* cu_q, const int32_t* kv_len, int64_t tokens, int64_t seqs, int64_t max_q,
     int64_t heads, int64_t kv_heads, int64_t dim, int64_t pages, int64_t page, int64_t width,
@@ -588,7 +829,7 @@ BD_EXPORT int bitdelta_paged_attention(
     return BITDELTA_ERR_SHAPE;
   if (tokens == 0 || seqs == 0 || max_q == 0) return BITDELTA_OK;
   if (!q || !k_cache || !v_cache || (!table && width > 0) || !cu_q || !kv_len || !out ||
-      (k_scale != nullptr) != (v_scale != nullptr))
+      !scales_ok(k_scale, v_scale, bits))
     return BITDELTA_ERR_NULL;
   if (!aligned2(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) ||
       !aligned16(v_scale) || !aligned4(table) || !aligned4(cu_q) || !aligned4(kv_len) ||
@@ -598,12 +839,12 @@ BD_EXPORT int bitdelta_paged_attention(
   const size_t need = bd::paged_attention_workspace(a);
   if (need > 0 && (!workspace || workspace_bytes < need)) return BITDELTA_ERR_WORKSPACE;
   const size_t rows = (size_t)pages * (size_t)page * (size_t)kv_heads;
-  const size_t cbytes = rows * (size_t)dim * (k_scale ? 1u : 2u);
+  const size_t cbytes = cache_bytes(rows, dim, bits), sbytes = scale_bytes(rows, dim, bits);
   const void* outs[2] = {out, need ? workspace : nullptr};
   const size_t outn[2] = {(size_t)(tokens * heads * dim) * 2u, need};
   const void* ins[8] = {q, k_cache, v_cache, k_scale, v_scale, table, cu_q, kv_len};
   const size_t inn[8] = {span(tokens, q_token_stride, heads, q_head_stride, dim), cbytes, cbytes,
-                         rows, rows, (size_t)(seqs * width) * 4u, (size_t)(seqs + 1) * 4u,
+                         sbytes, sbytes, (size_t)(seqs * width) * 4u, (size_t)(seqs + 1) * 4u,
                          (size_t)seqs * 4u};
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 8; ++j)
@@ -623,6 +864,7 @@ BD_EXPORT int bitdelta_paged_attention(
   a.cu_q = cu_q;
   a.kv_len = kv_len;
   a.pages = pages;
+  a.bits = bits;
   // a window that no sequence can fill hides nothing; what is left keeps
   // positions minus the window inside an int
   a.window = (int)(window < width * page ? window : 0);
@@ -630,6 +872,33 @@ BD_EXPORT int bitdelta_paged_attention(
   a.out = out;
   a.partial = static_cast<float*>(workspace);
   return status_of(bd::launch_paged_attention(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+BD_EXPORT int bitdelta_paged_attention(
+    const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+    const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* table,
+    const int32_t* cu_q, const int32_t* kv_len, int64_t tokens, int64_t seqs, int64_t max_q,
+    int64_t heads, int64_t kv_heads, int64_t dim, int64_t pages, int64_t page, int64_t width,
+    float scale, int64_t window, uint16_t* out, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  return paged_attention(k_scale ? 8 : 16, q, q_token_stride, q_head_stride, k_cache, v_cache,
+                         k_scale, v_scale, table, cu_q, kv_len, tokens, seqs, max_q, heads,
+                         kv_heads, dim, pages, page, width, scale, window, out, workspace,
+                         workspace_bytes, stream);
+}
+
+BD_EXPORT int bitdelta_paged_attention_4bit(
+    const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+    const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* table,
+    const int32_t* cu_q, const int32_t* kv_len, int64_t tokens, int64_t seqs, int64_t max_q,
+    int64_t heads, int64_t kv_heads, int64_t dim, int64_t pages, int64_t page, int64_t width,
+    float scale, int64_t window, uint16_t* out, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  return paged_attention(4, q, q_token_stride, q_head_stride, k_cache, v_cache, k_scale, v_scale,
+                         table, cu_q, kv_len, tokens, seqs, max_q, heads, kv_heads, dim, pages,
+                         page, width, scale, window, out, workspace, workspace_bytes, stream);
 }
 
 BD_EXPORT int bitdelta_probe_stream_read(const void* src, size_t bytes, int32_t workgroups,

@@ -1346,7 +1346,8 @@ size_t paged_attention_workspace(const AttnArgs& a) {
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t s) {
-  const bool q8 = a.scale[0] != nullptr;
+  if (a.bits == 4) return launch_attention_4bit(a, s);
+  const bool q8 = a.bits == 8;
   if (a.dim == 64) return q8 ? run<64, true>(a, s) : run<64, false>(a, s);
   return q8 ? run<128, true>(a, s) : run<128, false>(a, s);
 }

@@ -1,16 +1,18 @@
-// The paged key/value cache: rows [dim] of one head and token, in bf16 or in
-// e4m3 with one power-of-two scale per row.
+// The paged key/value cache: rows [dim] of one head and token, in bf16, in
+// e4m3 with one power-of-two scale per row, or in e2m1 with one per 32 dims.
 //
-// Both kernels move each row once and are bound by HBM (2 bytes a value on
-// the bf16 side, 2 or 1 + 1/dim on the cache's) or, for a batch of single
-// tokens, by the launch.  dim / 8 neighbouring lanes hold a row: one 16-byte
-// access a lane on the bf16 side, and the row's largest magnitude by lane
-// exchanges, so a row needs no LDS.  Neighbouring rows of a token are its
+// The kernels move each row once and are bound by HBM (2 bytes a value on the
+// bf16 side, 2, 1 + 1/dim or 1/2 + 1/32 on the cache's) or, for a batch of
+// single tokens, by the launch.  dim / 8 neighbouring lanes hold a row: one
+// 16-byte access a lane on the bf16 side, and a group's largest magnitude by
+// lane exchanges, so a row needs no LDS.  Neighbouring rows of a token are its
 // heads, contiguous on the side of the tokens.  64 tokens into 8 bits take 3.3
 // us, 2048 5.9 us, 16001 back 20.6 us (4.8 TB/s; a copy reaches 4.9).
 #include "common.h"
+#include "e2m1.h"
 #include "e4m3.h"
 #include "layer.h"
+#include "rotary.h"
 
 namespace bd {
 namespace {
@@ -22,9 +24,8 @@ struct Place {
 };
 
 template <int D>
-__device__ __forceinline__ bool place(const KvArgs& a, Place& p) {
+__device__ __forceinline__ bool place(const KvArgs& a, int64_t i, Place& p) {
   constexpr int L = D / 8;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int per = 2 * a.heads * L;
   p.token = i / per;
   if (p.token >= a.tokens) return false;
@@ -40,47 +41,89 @@ __device__ __forceinline__ bool place(const KvArgs& a, Place& p) {
   return true;
 }
 
-template <int D, bool Q8>
-__global__ __launch_bounds__(256) void kv_write_kernel(const KvArgs a) {
-  Place p;
-  if (!place<D>(a, p) || p.row < 0) return;  // whole rows leave together
-  const int w = p.which;
-  const u32x4 v = *reinterpret_cast<const u32x4_any*>(
-      a.src[w] + p.token * a.token_stride[w] + p.head * a.head_stride[w] + p.piece * 8);
-  if (!Q8) {
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.cache[w]) + p.row * D + p.piece * 8) = v;
-    return;
-  }
-  float f[8], m = 0.f;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    f[2 * d] = hold_e4m3(lo16(v[d]));
-    f[2 * d + 1] = hold_e4m3(hi16(v[d]));
-    m = fmaxf(m, fmaxf(fabsf(f[2 * d]), fabsf(f[2 * d + 1])));
-  }
-#pragma unroll
-  for (int o = 1; o < D / 8; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-  const uint32_t sb = scale_byte(m);
-  const float is = inv_scale(sb);
-  const u32x2 o = {pack_e4m3(f[0] * is, f[1] * is, f[2] * is, f[3] * is),
-                   pack_e4m3(f[4] * is, f[5] * is, f[6] * is, f[7] * is)};
-  *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.cache[w]) + p.row * D + p.piece * 8) = o;
-  if (p.piece == 0) a.scale[w][p.row] = (uint8_t)sb;
+__device__ __forceinline__ const uint16_t* source(const KvArgs& a, const Place& p) {
+  return a.src[p.which] + p.token * a.token_stride[p.which] + p.head * a.head_stride[p.which];
 }
 
-template <int D, bool Q8>
+__device__ __forceinline__ void to_floats(u32x4 v, float (&f)[8]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    f[2 * d] = lo16(v[d]);
+    f[2 * d + 1] = hi16(v[d]);
+  }
+}
+
+// Eight values of a row into the cache in 8 or 4 bits.
+template <int D, int BITS>
+__device__ __forceinline__ void put(const KvArgs& a, const Place& p, float (&f)[8]) {
+  const int w = p.which;
+  if constexpr (BITS == 8) {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[e] = hold_e4m3(f[e]);
+      m = fmaxf(m, fabsf(f[e]));
+    }
+#pragma unroll
+    for (int o = 1; o < D / 8; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+    const uint32_t sb = scale_byte(m);
+    const float is = inv_scale(sb);
+    const u32x2 o = {pack_e4m3(f[0] * is, f[1] * is, f[2] * is, f[3] * is),
+                     pack_e4m3(f[4] * is, f[5] * is, f[6] * is, f[7] * is)};
+    *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.cache[w]) + p.row * D + p.piece * 8) = o;
+    if (p.piece == 0) a.scale[w][p.row] = (uint8_t)sb;
+  } else {
+    uint32_t m = 0u;   // a magnitude's bits order as it does, a NaN's last
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[e] = hold_e2m1(f[e]);
+      m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+    }
+#pragma unroll
+    for (int o = 1; o < kGroup4 / 8; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+    const uint32_t sb = scale_byte4(m);
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.cache[w]) + p.row * (D / 2) +
+                                 p.piece * 4) =
+        sb == kNanScale ? 0u : pack_e2m1(f, __uint_as_float(sb << 23));
+    if (p.piece % (kGroup4 / 8) == 0)
+      a.scale[w][p.row * (D / kGroup4) + p.piece / (kGroup4 / 8)] = (uint8_t)sb;
+  }
+}
+
+template <int D, int BITS>
+__global__ __launch_bounds__(256) void kv_write_kernel(const KvArgs a) {
+  Place p;
+  // whole rows leave together
+  if (!place<D>(a, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, p) || p.row < 0) return;
+  const u32x4 v = *reinterpret_cast<const u32x4_any*>(source(a, p) + p.piece * 8);
+  if constexpr (BITS == 16) {
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.cache[p.which]) + p.row * D + p.piece * 8) =
+        v;
+  } else {
+    float f[8];
+    to_floats(v, f);
+    put<D, BITS>(a, p, f);
+  }
+}
+
+template <int D, int BITS>
 __global__ __launch_bounds__(256) void kv_read_kernel(const KvArgs a) {
   Place p;
-  if (!place<D>(a, p)) return;
+  if (!place<D>(a, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, p)) return;
   const int w = p.which;
   u32x4 v = {0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};  // no such slot: NaN
   if (p.row >= 0) {
-    if (Q8) {
+    if constexpr (BITS == 8) {
       const u32x2 c = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.cache[w]) +
                                                       p.row * D + p.piece * 8);
       const float s = __uint_as_float((uint32_t)a.scale[w][p.row] << 23);
       v = u32x4{bf16x2_of_e4m3<false>(c[0], s), bf16x2_of_e4m3<true>(c[0], s),
                 bf16x2_of_e4m3<false>(c[1], s), bf16x2_of_e4m3<true>(c[1], s)};
+    } else if constexpr (BITS == 4) {
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(
+          static_cast<const uint8_t*>(a.cache[w]) + p.row * (D / 2) + p.piece * 4);
+      const uint32_t sb = a.scale[w][p.row * (D / kGroup4) + p.piece / (kGroup4 / 8)];
+      v = bf16x8_of_e2m1(c, __uint_as_float(sb << 23));
     } else {
       v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.cache[w]) + p.row * D +
                                           p.piece * 8);
@@ -89,9 +132,80 @@ __global__ __launch_bounds__(256) void kv_read_kernel(const KvArgs a) {
   *reinterpret_cast<u32x4*>(a.dst[w] + (p.token * a.heads + p.head) * D + p.piece * 8) = v;
 }
 
+// Eight values of a row of k, turned by its token's angles.
+template <int D, bool INTERLEAVED>
+__device__ __forceinline__ void turn(const RotaryArgs& r, int64_t token, const uint16_t* row,
+                                     int d0, float (&f)[8]) {
+  if (d0 >= r.rot) return;
+  const float* t = table_row(r.table, r.length, r.rot, r.positions[token]);
+  const int half = r.rot >> 1;
+  if constexpr (INTERLEAVED) {
+    const int n = min((r.rot - d0) >> 1, 4);
+    Angles<4> g;
+    g.load(t ? t + d0 : nullptr, n);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) {
+        const float a = f[2 * e], b = f[2 * e + 1];
+        f[2 * e] = turned_first(a, b, g.c[e], g.s[e]);
+        f[2 * e + 1] = turned_second(a, b, g.c[e], g.s[e]);
+      }
+  } else if (half % 8 == 0) {   // the eight are all first or all second members
+    const bool second = d0 >= half;
+    const int pair = second ? d0 - half : d0;
+    float o[8];
+    to_floats(*reinterpret_cast<const u32x4_any*>(row + (second ? pair : pair + half)), o);
+    Angles<8> g;
+    g.load(t ? t + 2 * pair : nullptr, 8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      f[e] = second ? turned_second(o[e], f[e], g.c[e], g.s[e])
+                    : turned_first(f[e], o[e], g.c[e], g.s[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int d = d0 + e;
+      if (d < r.rot) {
+        const bool second = d >= half;
+        const int pair = second ? d - half : d;
+        const float o = __uint_as_float((uint32_t)row[second ? pair : pair + half] << 16);
+        const float c = t ? t[2 * pair] : NAN, s = t ? t[2 * pair + 1] : NAN;
+        f[e] = second ? turned_second(o, f[e], c, s) : turned_first(f[e], o, c, s);
+      }
+    }
+  }
+}
+
+// The first kv_groups workgroups put rows into the cache, the others turn the
+// queries: one launch for what a step has between its QKV product and its
+// attention.
+template <int D, int BITS, bool INTERLEAVED>
+__global__ __launch_bounds__(256) void kv_append_kernel(const KvArgs a, const RotaryArgs r,
+                                                        const unsigned kv_groups) {
+  if (blockIdx.x >= kv_groups) {
+    rotate_unit<INTERLEAVED>(r, (int)((blockIdx.x - kv_groups) * 256 + threadIdx.x));
+    return;
+  }
+  Place p;
+  if (!place<D>(a, (int64_t)blockIdx.x * 256 + threadIdx.x, p) || p.row < 0) return;
+  const uint16_t* row = source(a, p);
+  float f[8];
+  to_floats(*reinterpret_cast<const u32x4_any*>(row + p.piece * 8), f);
+  if (p.which == 0) turn<D, INTERLEAVED>(r, p.token, row, p.piece * 8, f);
+  if constexpr (BITS == 16) {
+    u32x4 v;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d] = cvt_pk_bf16(f[2 * d], f[2 * d + 1]);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.cache[p.which]) + p.row * D + p.piece * 8) =
+        v;
+  } else {
+    put<D, BITS>(a, p, f);
+  }
+}
+
 // A launch takes fewer than 2^32 threads: more tokens than that go in several
 // launches, of 2^31 threads at most.
-template <int D, bool Q8, bool WRITE>
+template <int D, int BITS, bool WRITE>
 hipError_t run(const KvArgs& a, hipStream_t s) {
   const int64_t per = (int64_t)2 * a.heads * (D / 8);   // threads of a token
   const int64_t most = (int64_t(1) << 31) / per;
@@ -104,24 +218,61 @@ hipError_t run(const KvArgs& a, hipStream_t s) {
       else b.dst[w] += at * a.heads * D;
     }
     const unsigned grid = (unsigned)((b.tokens * per + 255) / 256);
-    if (WRITE) kv_write_kernel<D, Q8><<<grid, 256, 0, s>>>(b);
-    else kv_read_kernel<D, Q8><<<grid, 256, 0, s>>>(b);
+    if (WRITE) kv_write_kernel<D, BITS><<<grid, 256, 0, s>>>(b);
+    else kv_read_kernel<D, BITS><<<grid, 256, 0, s>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <bool WRITE>
+template <int D, int BITS>
+hipError_t run_append(const KvArgs& a, RotaryArgs r, hipStream_t s) {
+  const int64_t per = (int64_t)2 * a.heads * (D / 8), per_q = rotary_plan(r);
+  const int64_t most = (int64_t(1) << 30) / (per > per_q ? per : per_q);
+  for (int64_t at = 0; at < a.tokens; at += most) {
+    KvArgs b = a;
+    RotaryArgs q = r;
+    b.tokens = q.tokens = a.tokens - at < most ? a.tokens - at : most;
+    b.slots += at;
+    q.positions += at;
+    for (int w = 0; w < 2; ++w) b.src[w] += at * a.token_stride[w];
+    q.x += at * r.x_token_stride;
+    q.out += at * r.out_token_stride;
+    const unsigned kv = (unsigned)((b.tokens * per + 255) / 256);
+    const unsigned grid = kv + (unsigned)((b.tokens * per_q + 255) / 256);
+    if (r.interleaved) kv_append_kernel<D, BITS, true><<<grid, 256, 0, s>>>(b, q, kv);
+    else kv_append_kernel<D, BITS, false><<<grid, 256, 0, s>>>(b, q, kv);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int D, bool WRITE>
 hipError_t pick(const KvArgs& a, hipStream_t s) {
-  const bool q8 = a.scale[0] != nullptr;
-  if (a.dim == 64) return q8 ? run<64, true, WRITE>(a, s) : run<64, false, WRITE>(a, s);
-  return q8 ? run<128, true, WRITE>(a, s) : run<128, false, WRITE>(a, s);
+  return a.bits == 16  ? run<D, 16, WRITE>(a, s)
+         : a.bits == 8 ? run<D, 8, WRITE>(a, s)
+                       : run<D, 4, WRITE>(a, s);
+}
+
+template <int D>
+hipError_t pick_append(const KvArgs& a, const RotaryArgs& q, hipStream_t s) {
+  return a.bits == 16  ? run_append<D, 16>(a, q, s)
+         : a.bits == 8 ? run_append<D, 8>(a, q, s)
+                       : run_append<D, 4>(a, q, s);
 }
 
 }  // namespace
 
-hipError_t launch_kv_write(const KvArgs& a, hipStream_t s) { return pick<true>(a, s); }
-hipError_t launch_kv_read(const KvArgs& a, hipStream_t s) { return pick<false>(a, s); }
+hipError_t launch_kv_write(const KvArgs& a, hipStream_t s) {
+  return a.dim == 64 ? pick<64, true>(a, s) : pick<128, true>(a, s);
+}
+hipError_t launch_kv_read(const KvArgs& a, hipStream_t s) {
+  return a.dim == 64 ? pick<64, false>(a, s) : pick<128, false>(a, s);
+}
+hipError_t launch_kv_append(const KvArgs& a, const RotaryArgs& q, hipStream_t s) {
+  return a.dim == 64 ? pick_append<64>(a, q, s) : pick_append<128>(a, q, s);
+}
 
 }  // namespace bd

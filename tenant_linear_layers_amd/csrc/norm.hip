@@ -238,7 +238,165 @@ hipError_t pick(const NormArgs& a, hipStream_t s) {
   return rows_of<1024, 0, RES, MX>(a, s);
 }
 
+// ------------------------------------------------------------------ around a block
+// Eight values of w (1 past the row, where there is no w).
+__device__ __forceinline__ void weight8(const uint16_t* w, int n, float (&f)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 1.f;
+    return;
+  }
+  const u32x4 v = n >= 8 ? ld8(w) : ld_some(w, n);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    f[2 * d] = lo16(v[d]);
+    f[2 * d + 1] = hi16(v[d]);
+  }
+}
+
+// h = residual + alpha * gate * x * inv * post, of which x comes in and h goes
+// out as float32 and, rounded, to memory.
+__device__ __forceinline__ void add_block(const BlockNormArgs& a, int64_t row, int col, int n,
+                                          float inv, float (&f)[8]) {
+  float p[8], g[8], r[8];
+  weight8(a.post ? a.post + col : nullptr, n, p);
+  weight8(a.gate ? a.gate + row * a.g_stride + col : nullptr, n, g);
+  weight8(a.residual + row * a.r_stride + col, n, r);
+  u32x4 o;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e] * inv * p[e] * g[e], a.alpha, r[e]);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) o[d] = cvt_pk_bf16(f[2 * d], f[2 * d + 1]);
+  uint16_t* h = a.h + row * a.cols + col;
+  if (n >= 8) st8(h, o);
+  else st_some(h, o, n);
+}
+
+__device__ __forceinline__ void put_block(const BlockNormArgs& a, int64_t row, int col, int n,
+                                          float inv, const float (&f)[8]) {
+  float w[8];
+  weight8(a.w + col, n, w);
+  u32x4 o;
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+    o[d] = cvt_pk_bf16(f[2 * d] * inv * w[2 * d], f[2 * d + 1] * inv * w[2 * d + 1]);
+  uint16_t* y = a.y + row * a.cols + col;
+  if (n >= 8) st8(y, o);
+  else st_some(y, o, n);
+}
+
+// The norm after a block and the one before the next: as rms_norm_kernel, with
+// a row's x and then its h in registers and a sum of squares of each, so every
+// value is read once.
+template <int T, int CH>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_block_kernel(const BlockNormArgs a) {
+  __shared__ float red[2][T / kWave];
+  const int t = T < 256 ? threadIdx.x & (T - 1) : threadIdx.x;
+  const int64_t row = T < 256 ? (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T : blockIdx.x;
+  if (T < 256 && row >= a.rows) return;  // whole waves
+  float f[CH][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = (c * T + t) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[c][e] = 0.f;
+    if (col < a.cols)
+      load_sum<false>(a.x + row * a.x_stride + col, nullptr, nullptr, a.cols - col, f[c]);
+  }
+  float inv = 1.f;
+  if (a.post) {   // the same for all
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(f[c][e], f[c][e], ss);
+    inv = inverse<false>(row_sum<T>(ss, red[0]), a.cols, a.eps).hi;
+  }
+  ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = (c * T + t) * 8;
+    if (col < a.cols) {
+      add_block(a, row, col, a.cols - col, inv, f[c]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(f[c][e], f[c][e], ss);
+    }
+  }
+  inv = inverse<false>(row_sum<T>(ss, red[1]), a.cols, a.eps).hi;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = (c * T + t) * 8;
+    if (col < a.cols) put_block(a, row, col, a.cols - col, inv, f[c]);
+  }
+}
+
+// Rows too long for the registers of one workgroup: x is read three times.
+__global__ __launch_bounds__(1024) void rms_norm_block_long_kernel(const BlockNormArgs a) {
+  __shared__ float red[2][16];
+  const int64_t row = blockIdx.x;
+  const uint16_t* x = a.x + row * a.x_stride;
+  float f[8], ss = 0.f, inv = 1.f;
+  auto value = [&](int64_t col) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    load_sum<false>(x + col, nullptr, nullptr, (int)(a.cols - col), f);
+  };
+  if (a.post) {
+    for (int64_t col = threadIdx.x * 8; col < a.cols; col += 8192) {
+      value(col);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+    }
+    inv = inverse<false>(row_sum<1024>(ss, red[0]), a.cols, a.eps).hi;
+  }
+  ss = 0.f;
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 8192) {
+    value(col);
+    add_block(a, row, (int)col, (int)(a.cols - col), inv, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+  }
+  const float inv2 = inverse<false>(row_sum<1024>(ss, red[1]), a.cols, a.eps).hi;
+  for (int64_t col = threadIdx.x * 8; col < a.cols; col += 8192) {
+    value(col);
+    add_block(a, row, (int)col, (int)(a.cols - col), inv, f);   // the same bits again
+    put_block(a, row, (int)col, (int)(a.cols - col), inv2, f);
+  }
+}
+
+template <int T, int CH>
+hipError_t blocks_of(const BlockNormArgs& a, hipStream_t s) {
+  constexpr int kBlock = T < 256 ? 256 : T, kRows = kBlock / T;   // of a workgroup
+  constexpr int64_t kMost = kMostThreads / T;
+  for (int64_t at = 0; at < a.rows; at += kMost) {
+    BlockNormArgs b = a;
+    b.rows = a.rows - at < kMost ? a.rows - at : kMost;
+    b.x += at * a.x_stride;
+    b.residual += at * a.r_stride;
+    if (a.gate) b.gate += at * a.g_stride;
+    b.h += at * a.cols;
+    b.y += at * a.cols;
+    const unsigned grid = (unsigned)((b.rows + kRows - 1) / kRows);
+    if constexpr (CH > 0) rms_norm_block_kernel<T, CH><<<grid, kBlock, 0, s>>>(b);
+    else rms_norm_block_long_kernel<<<grid, kBlock, 0, s>>>(b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
+
+// Threads of a row: as for the norm above.
+hipError_t launch_rms_norm_block(const BlockNormArgs& a, hipStream_t s) {
+  if (a.cols <= 512) return blocks_of<64, 1>(a, s);
+  if (a.cols <= 1024) return blocks_of<64, 2>(a, s);
+  if (a.cols <= 2048) return blocks_of<256, 1>(a, s);
+  if (a.cols <= 4096) return blocks_of<512, 1>(a, s);
+  if (a.cols <= 8192) return blocks_of<1024, 1>(a, s);
+  if (a.cols <= 16384) return blocks_of<1024, 2>(a, s);
+  return blocks_of<1024, 0>(a, s);
+}
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
   if (a.scale) return a.residual ? pick<true, true>(a, s) : pick<false, true>(a, s);
