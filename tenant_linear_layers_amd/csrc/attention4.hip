@@ -170,14 +170,19 @@ __global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnAr
   int blocks = -1;   // lane 2 i + h: rows / 16 of the cache for half h of step i (mod 32)
   const int vpiece = lane % GROUPS;                    // V's group of the lane
   const int vkey = lane / GROUPS;                      // and its row, of the first load
-  const int koff = n * GROUPS + g4 % GROUPS;           // group of K of 16 rows
+  // its group of K of 16 rows, and its place among theirs of V
+  const uint32_t koff = n * GROUPS + g4 % GROUPS, voff = lane % (16 * GROUPS);
   char* vput = vst + vkey * ROWL + vpiece * 64;
   const uint32_t vget =
       lds_address(vst + (4 * g4 + (n >> 2)) * ROWL + ((n >> 1) & 1) * 16 + 8 * (n & 1));
 
+  // A step's scales come with one load, of K's rows to lanes 0..31 and of V's to
+  // the others, and go from there to the lanes that want them: loads of their
+  // own for every operand take 4 us of 80 (40 sequences of 8000 keys).
+  const uint8_t* sbase = lane < 32 ? a.scale[0] : a.scale[1];
   struct Rows {
     u32x4 k[2], v[VLOADS];
-    uint32_t ks[2], vs[VLOADS];
+    uint32_t sc;
   };
   auto fetch = [&](int i, Rows& r) {
     if ((i & 31) == 0) {
@@ -193,34 +198,19 @@ __global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnAr
           bad |= key + 16 > lo;
       }
     }
-    // Rows that are not there, of a step's end and of no page, lie past the
-    // resource: their scales are read as 0, 2^-127, and V is finite under a weight
-    // of zero.  So are V's scales below lo.
-    const int key0 = kbeg + 32 * NW * i;
+    // halves that are not there are read from block 0
+    int blk[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int blk = __builtin_amdgcn_readlane(blocks, 2 * (i & 31) + h);
-      const int rows = __builtin_amdgcn_readfirstlane(
-          blk < 0 ? 0 : min(max(hi - key0 - 16 * h, 0), 16));
-      const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(max(blk, 0)) * 16;
-      const uint8_t* v = a.cache[1] + row * ROWB;
-      const uint8_t* vs = a.scale[1] + row * GROUPS;
-      r.k[h] = bload128(a.cache[0] + row * ROWB, rows * ROWB, koff * 16, 0);
-      r.ks[h] = bload8(a.scale[0] + row * GROUPS, rows * GROUPS, koff, 0);
-      constexpr int kPast = 1 << 30;
-      if constexpr (D == 128) {
-        const bool below = key0 + 16 * h + vkey < lo;
-        r.v[h] = bload128(v, rows * ROWB, lane * 16, 0);
-        r.vs[h] = bload8(vs, rows * GROUPS, below ? kPast : lane, 0);
-      } else {   // half of the lanes; the others read 0
-        const bool mine = lane >= 32 == (h == 1);
-        const u32x4 got = bload128(v, rows * ROWB, mine ? (lane & 31) * 16 : kPast, 0);
-        const uint32_t sc =
-            bload8(vs, rows * GROUPS, mine && key0 + vkey >= lo ? lane & 31 : kPast, 0);
-        r.v[0] = h ? r.v[0] | got : got;
-        r.vs[0] = h ? r.vs[0] | sc : sc;
-      }
+      blk[h] = max(__builtin_amdgcn_readlane(blocks, 2 * (i & 31) + h), 0);
+      const int64_t row = (int64_t)blk[h] * (16 * ROWB);
+      r.k[h] = ld128(a.cache[0] + row + koff * 16);
+      if (D == 128 || lane >= 32 == (h == 1))   // with 64 dims half of the lanes
+        r.v[D == 128 ? h : 0] = ld128(a.cache[1] + row + voff * 16);
     }
+    const uint8_t* sp =
+        sbase + (int64_t)(lane & 16 ? blk[1] : blk[0]) * (16 * GROUPS) + (lane & 15) * GROUPS;
+    r.sc = D == 128 ? ld32(sp) : *reinterpret_cast<const uint16_t*>(sp);
   };
 
   f32x4 acc[D / 16];
@@ -228,26 +218,42 @@ __global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnAr
 
   auto step = [&](int i, const Rows& r) {
     const int key0 = kbeg + 32 * NW * i;
+    const bool ends = key0 < lo || key0 + 32 > hi;   // rows of it do not count
+    uint32_t ks[2], vs[VLOADS];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      ks[h] = (uint32_t)__shfl((int)r.sc, 16 * h + n) >> (8 * (g4 % GROUPS));
+#pragma unroll
+    for (int h = 0; h < VLOADS; ++h)
+      vs[h] = (uint32_t)__shfl((int)r.sc, 32 + 16 * h + vkey) >> (8 * vpiece) & 0xFFu;
     float s[8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       f32x4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int p = 0; p < D / 64; ++p) z = mfma16_fp4(r.k[h], qf[p], z, r.ks[h], qs[p]);
+      for (int p = 0; p < D / 64; ++p) z = mfma16_fp4(r.k[h], qf[p], z, ks[h], qs[p]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[4 * h + e] = z[e] * a.scale_log2;
+      for (int e = 0; e < 4; ++e) s[4 * h + e] = z[e];
+    }
+    if (ends) {   // the smallest scale: finite under their weights of zero
+      asm volatile("");   // a branch, not comparisons in every step
+#pragma unroll
+      for (int h = 0; h < VLOADS; ++h) {
+        const int key = key0 + 16 * h + vkey;
+        vs[h] = key >= lo && key < hi ? vs[h] : 0u;
+      }
     }
     // V as bf16 into LDS
 #pragma unroll
     for (int h = 0; h < VLOADS; ++h) {
-      const float sc = __uint_as_float(r.vs[h] << 23);
+      const float sc = __uint_as_float(vs[h] << 23);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *reinterpret_cast<u32x4*>(vput + 16 * h * ROWL + 16 * j) = bf16x8_of_e2m1(r.v[h][j], sc);
     }
     // a mask only where some row of the tile sees part of the step
-    if (key0 + 32 > t.all_hi || key0 < t.all_lo || key0 + 32 > hi || key0 < lo) {
-      asm volatile("");   // a branch: without it the comparisons are made in every step
+    if (ends || key0 + 32 > t.all_hi || key0 < t.all_lo) {
+      asm volatile("");
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int j = key0 + 16 * (e >> 2) + 4 * g4 + (e & 3);
@@ -257,6 +263,7 @@ __global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnAr
     float top = s[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
+    top *= a.scale_log2;
     // The reference moves only when a score passes it by 2^6 or more: until
     // then the weights stay below 2^6, far from the limits of float32 and
     // bf16, and no lane exchange or rescaling is needed.
@@ -274,8 +281,8 @@ __global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnAr
     u32x4 pf;
 #pragma unroll
     for (int e = 0; e < 8; e += 2)
-      pf[e >> 1] = weights(__builtin_amdgcn_exp2f(s[e] - ref),
-                           __builtin_amdgcn_exp2f(s[e + 1] - ref), l);
+      pf[e >> 1] = weights(__builtin_amdgcn_exp2f(fmaf(s[e], a.scale_log2, -ref)),
+                           __builtin_amdgcn_exp2f(fmaf(s[e + 1], a.scale_log2, -ref)), l);
     u32x4 vf[4];   // of four tiles of 16 dims
     read_tr16_4<0, 16 * ROWL>(vget, vf);
 #pragma unroll
@@ -304,8 +311,8 @@ __global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnAr
       Rows r[2];
       fetch(0, r[0]);
       for (int i = 0; i < steps; i += 2) {
-        // past the last step there are no rows left, and loads that read nothing:
-        // with a branch here a step would have to wait for the next one's
+        // past the last step there are no rows left to count: with a branch here a
+        // step would have to wait for the next one's loads
         fetch(i + 1, r[1]);
         step(i, r[0]);
         fetch(i + 2, r[0]);
