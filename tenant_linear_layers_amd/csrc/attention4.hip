@@ -176,6 +176,9 @@ __global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnAr
   const uint32_t vget =
       lds_address(vst + (4 * g4 + (n >> 2)) * ROWL + ((n >> 1) & 1) * 16 + 8 * (n & 1));
 
+  // V's rows, whole lines by a load, are read past the caches' turn of use: K's,
+  // whose lines several parts of a load want, stay longer (64 sequences of up to
+  // 16000 keys 86 us, both so 94, neither 102; 4 of 4097 keys 16.0, 14.5 and 15.7).
   // A step's scales come with one load, of K's rows to lanes 0..31 and of V's to
   // the others, and go from there to the lanes that want them: loads of their
   // own for every operand take 4 us of 80 (40 sequences of 8000 keys).
@@ -206,7 +209,8 @@ __global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnAr
       const int64_t row = (int64_t)blk[h] * (16 * ROWB);
       r.k[h] = ld128(a.cache[0] + row + koff * 16);
       if (D == 128 || lane >= 32 == (h == 1))   // with 64 dims half of the lanes
-        r.v[D == 128 ? h : 0] = ld128(a.cache[1] + row + voff * 16);
+        r.v[D == 128 ? h : 0] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(a.cache[1] + row + voff * 16));
     }
     const uint8_t* sp =
         sbase + (int64_t)(lane & 16 ? blk[1] : blk[0]) * (16 * GROUPS) + (lane & 15) * GROUPS;
@@ -401,7 +405,9 @@ __global__ __launch_bounds__(256, 2) void attend4_many_kernel(const AttnArgs a, 
   constexpr int LPR = ROW / (4 * W);                 // lanes a row
   constexpr int MINE = 64 / LPR;                     // rows of a step, by one wave
   // One workgroup's matrix products go first and the other's softmax fills in.
-  constexpr bool FIRST = D == 128;
+  // Not for tiles of 64 rows of 64 dims (24 mixed sequences 43.4 us, with it 44.1; a
+  // prompt of 2048 in tiles of 128 55.5 and 52.1).
+  constexpr bool FIRST = D == 128 || RG == 4;
   __shared__ __attribute__((aligned(16))) char smem[M::SMEM];
 
   Item it;

@@ -17,28 +17,40 @@
 namespace bd {
 namespace {
 
-// One lane's place: which cache (0 k, 1 v), token, head and the eight values.
+// Thread i's place: which cache (0 k, 1 v), token, head and the eight values.
 struct Place {
   int which, head, piece;
   int64_t token, row;  // row of the cache, or -1 for a slot outside it
 };
 
 template <int D>
-__device__ __forceinline__ bool place(const KvArgs& a, int64_t i, Place& p) {
+__device__ __forceinline__ bool place(const KvArgs& a, int i, Place& p) {
   constexpr int L = D / 8;
-  const int per = 2 * a.heads * L;
-  p.token = i / per;
-  if (p.token >= a.tokens) return false;
-  const int j = (int)(i - p.token * per);
+  const int token = a.by_token.of(i);
+  const int j = i - token * a.by_token.by;
+  p.token = token;
   p.piece = j % L;
   p.which = j / L >= a.heads;
   p.head = j / L - (p.which ? a.heads : 0);
+  return token < a.tokens;
+}
+
+// The place's row of the cache: after the source's load, which does not wait for
+// the slot's.
+__device__ __forceinline__ void find_row(const KvArgs& a, Place& p) {
   const int slot = a.slots[p.token];
-  const int page = slot / a.page;
+  const int page = a.by_page.of(max(slot, 0));
   p.row = slot < 0 || slot >= a.n_slots
               ? -1
               : ((int64_t)page * a.heads + p.head) * a.page + (slot - page * a.page);
-  return true;
+}
+
+// The larger of a lane's value and its neighbour's, one or two lanes on in its
+// four.
+template <int STEP>
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  constexpr int kOther = STEP == 1 ? 0xB1 : 0x4E;   // lanes 1 0 3 2, lanes 2 3 0 1
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kOther, 0xF, 0xF, true));
 }
 
 __device__ __forceinline__ const uint16_t* source(const KvArgs& a, const Place& p) {
@@ -79,8 +91,7 @@ __device__ __forceinline__ void put(const KvArgs& a, const Place& p, float (&f)[
       f[e] = hold_e2m1(f[e]);
       m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);
     }
-#pragma unroll
-    for (int o = 1; o < kGroup4 / 8; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+    m = quad_max<2>(quad_max<1>(m));   // four lanes hold a group
     const uint32_t sb = scale_byte4(m);
     *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.cache[w]) + p.row * (D / 2) +
                                  p.piece * 4) =
@@ -93,9 +104,10 @@ __device__ __forceinline__ void put(const KvArgs& a, const Place& p, float (&f)[
 template <int D, int BITS>
 __global__ __launch_bounds__(256) void kv_write_kernel(const KvArgs a) {
   Place p;
-  // whole rows leave together
-  if (!place<D>(a, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, p) || p.row < 0) return;
+  if (!place<D>(a, (int)(blockIdx.x * 256 + threadIdx.x), p)) return;
   const u32x4 v = *reinterpret_cast<const u32x4_any*>(source(a, p) + p.piece * 8);
+  find_row(a, p);
+  if (p.row < 0) return;   // whole rows leave together
   if constexpr (BITS == 16) {
     *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.cache[p.which]) + p.row * D + p.piece * 8) =
         v;
@@ -109,7 +121,8 @@ __global__ __launch_bounds__(256) void kv_write_kernel(const KvArgs a) {
 template <int D, int BITS>
 __global__ __launch_bounds__(256) void kv_read_kernel(const KvArgs a) {
   Place p;
-  if (!place<D>(a, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, p)) return;
+  if (!place<D>(a, (int)(blockIdx.x * 256 + threadIdx.x), p)) return;
+  find_row(a, p);
   const int w = p.which;
   u32x4 v = {0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};  // no such slot: NaN
   if (p.row >= 0) {
@@ -187,11 +200,13 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvArgs a, const Ro
     return;
   }
   Place p;
-  if (!place<D>(a, (int64_t)blockIdx.x * 256 + threadIdx.x, p) || p.row < 0) return;
+  if (!place<D>(a, (int)(blockIdx.x * 256 + threadIdx.x), p)) return;
   const uint16_t* row = source(a, p);
   float f[8];
   to_floats(*reinterpret_cast<const u32x4_any*>(row + p.piece * 8), f);
   if (p.which == 0) turn<D, INTERLEAVED>(r, p.token, row, p.piece * 8, f);
+  find_row(a, p);
+  if (p.row < 0) return;   // whole rows leave together
   if constexpr (BITS == 16) {
     u32x4 v;
 #pragma unroll
@@ -203,14 +218,16 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvArgs a, const Ro
   }
 }
 
-// A launch takes fewer than 2^32 threads: more tokens than that go in several
-// launches, of 2^31 threads at most.
+// A thread's index is an int: more tokens than that go in several launches, of
+// 2^30 threads at most.
 template <int D, int BITS, bool WRITE>
 hipError_t run(const KvArgs& a, hipStream_t s) {
   const int64_t per = (int64_t)2 * a.heads * (D / 8);   // threads of a token
-  const int64_t most = (int64_t(1) << 31) / per;
+  const int64_t most = (int64_t(1) << 30) / per;
   for (int64_t at = 0; at < a.tokens; at += most) {
     KvArgs b = a;
+    b.by_token = divisor((int)per);
+    b.by_page = divisor(a.page);
     b.tokens = a.tokens - at < most ? a.tokens - at : most;
     b.slots += at;
     for (int w = 0; w < 2; ++w) {
@@ -233,6 +250,8 @@ hipError_t run_append(const KvArgs& a, RotaryArgs r, hipStream_t s) {
   for (int64_t at = 0; at < a.tokens; at += most) {
     KvArgs b = a;
     RotaryArgs q = r;
+    b.by_token = divisor((int)per);
+    b.by_page = divisor(a.page);
     b.tokens = q.tokens = a.tokens - at < most ? a.tokens - at : most;
     b.slots += at;
     q.positions += at;

@@ -95,6 +95,7 @@ struct KvArgs {
   int64_t token_stride[2], head_stride[2];
   int64_t tokens, n_slots;
   int heads, dim, page, bits;
+  Divisor by_token, by_page;   // threads of a token, page (set by the launcher)
 };
 hipError_t launch_kv_write(const KvArgs& a, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& a, hipStream_t stream);
