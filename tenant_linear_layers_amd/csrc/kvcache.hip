@@ -189,18 +189,19 @@ __device__ __forceinline__ void turn(const RotaryArgs& r, int64_t token, const u
   }
 }
 
-// The first kv_groups workgroups put rows into the cache, the others turn the
-// queries: one launch for what a step has between its QKV product and its
-// attention.
+// The first q_groups workgroups turn the queries, the others put rows into the
+// cache: one launch for what a step has between its QKV product and its
+// attention.  The queries, most of the bytes, go first: 2048 tokens of 64 heads
+// 16.2 us, the other way round 18.1 (16001 tokens 156 and 151).
 template <int D, int BITS, bool INTERLEAVED>
 __global__ __launch_bounds__(256) void kv_append_kernel(const KvArgs a, const RotaryArgs r,
-                                                        const unsigned kv_groups) {
-  if (blockIdx.x >= kv_groups) {
-    rotate_unit<INTERLEAVED>(r, (int)((blockIdx.x - kv_groups) * 256 + threadIdx.x));
+                                                        const unsigned q_groups) {
+  if (blockIdx.x < q_groups) {
+    rotate_unit<INTERLEAVED>(r, (int)(blockIdx.x * 256 + threadIdx.x));
     return;
   }
   Place p;
-  if (!place<D>(a, (int)(blockIdx.x * 256 + threadIdx.x), p)) return;
+  if (!place<D>(a, (int)((blockIdx.x - q_groups) * 256 + threadIdx.x), p)) return;
   const uint16_t* row = source(a, p);
   float f[8];
   to_floats(*reinterpret_cast<const u32x4_any*>(row + p.piece * 8), f);
@@ -258,10 +259,10 @@ hipError_t run_append(const KvArgs& a, RotaryArgs r, hipStream_t s) {
     for (int w = 0; w < 2; ++w) b.src[w] += at * a.token_stride[w];
     q.x += at * r.x_token_stride;
     q.out += at * r.out_token_stride;
-    const unsigned kv = (unsigned)((b.tokens * per + 255) / 256);
-    const unsigned grid = kv + (unsigned)((b.tokens * per_q + 255) / 256);
-    if (r.interleaved) kv_append_kernel<D, BITS, true><<<grid, 256, 0, s>>>(b, q, kv);
-    else kv_append_kernel<D, BITS, false><<<grid, 256, 0, s>>>(b, q, kv);
+    const unsigned turns = (unsigned)((b.tokens * per_q + 255) / 256);
+    const unsigned grid = turns + (unsigned)((b.tokens * per + 255) / 256);
+    if (r.interleaved) kv_append_kernel<D, BITS, true><<<grid, 256, 0, s>>>(b, q, turns);
+    else kv_append_kernel<D, BITS, false><<<grid, 256, 0, s>>>(b, q, turns);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -166,16 +166,9 @@ def _gate(gate, shape, dev: int):
     return _rows(gate, "gate", shape, dev)
 
 
-def rms_norm_block(x: torch.Tensor, residual: torch.Tensor, post_weight, weight: torch.Tensor,
-                   eps: float, gate=None, scale: float = 1.0, y=None, h=None, stream=None):
-    """(y, h) of a block's output x, around its end and before the next block:
-
-        u = x / sqrt(mean(x^2) + eps) * post_weight     (post_weight None: u = x)
-        h = residual + scale * gate * u                 (gate None: 1)
-        y = h / sqrt(mean(h^2) + eps) * weight
-
-    x, residual, y, h: bf16 [..., cols]; gate: bf16 of that shape or [cols];
-    post_weight, weight: bf16 [cols]; scale: finite."""
+def _block_checks(x, residual, post_weight, weight, gate, scale, y, h):
+    """(device, row strides of x, residual and gate) of a block norm's tensors,
+    or what is wrong with them."""
     dev = _device(x, "x")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be [..., cols]")
@@ -195,6 +188,38 @@ def rms_norm_block(x: torch.Tensor, residual: torch.Tensor, post_weight, weight:
                 raise ValueError(f"{name} must have x's shape")
     if not math.isfinite(scale):
         raise ValueError(f"scale must be finite, got {scale}")
+    return dev, xs, rs, gs
+
+
+def rms_norm_block(x: torch.Tensor, residual: torch.Tensor, post_weight, weight: torch.Tensor,
+                   eps: float, gate=None, scale: float = 1.0, y=None, h=None, stream=None):
+    """(y, h) of a block's output x, around its end and before the next block:
+
+        u = x / sqrt(mean(x^2) + eps) * post_weight     (post_weight None: u = x)
+        h = residual + scale * gate * u                 (gate None: 1)
+        y = h / sqrt(mean(h^2) + eps) * weight
+
+    x, residual, y, h: bf16 [..., cols]; gate: bf16 of that shape or [cols];
+    post_weight, weight: bf16 [cols]; scale: finite."""
+    gs = 0
+    try:
+        shape = x.shape
+        xs = rs = cols = shape[-1]
+        dev = x.get_device()
+        usual = (cols > 0 and dev >= 0 and x.dtype is _BF16 and x.is_contiguous() and
+                 residual.dtype is _BF16 and residual.shape == shape and
+                 residual.get_device() == dev and residual.is_contiguous() and
+                 weight.dtype is _BF16 and weight.get_device() == dev and
+                 weight.numel() == cols and weight.is_contiguous() and
+                 (post_weight is None or post_weight.dtype is _BF16 and
+                  post_weight.get_device() == dev and post_weight.numel() == cols and
+                  post_weight.is_contiguous()) and
+                 gate is None and y is None and h is None and math.isfinite(scale))
+    except (AttributeError, IndexError, TypeError):
+        usual = False
+    if not usual:
+        dev, xs, rs, gs = _block_checks(x, residual, post_weight, weight, gate, scale, y, h)
+        cols = x.shape[-1]
     with _at(dev, stream):
         y = torch.empty_like(x, memory_format=_ROWS) if y is None else y
         h = torch.empty_like(x, memory_format=_ROWS) if h is None else h
