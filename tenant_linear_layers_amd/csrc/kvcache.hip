@@ -17,10 +17,11 @@
 namespace bd {
 namespace {
 
-// Thread i's place: which cache (0 k, 1 v), token, head and the eight values.
+// Thread i's place: token, head and eight values, of k and of v (one row's place
+// for both, and two loads on their way).
 struct Place {
-  int which, head, piece;
-  int64_t token, row;  // row of the cache, or -1 for a slot outside it
+  int head, piece;
+  int64_t token, row;  // row of the caches, or -1 for a slot outside them
 };
 
 template <int D>
@@ -30,12 +31,11 @@ __device__ __forceinline__ bool place(const KvArgs& a, int i, Place& p) {
   const int j = i - token * a.by_token.by;
   p.token = token;
   p.piece = j % L;
-  p.which = j / L >= a.heads;
-  p.head = j / L - (p.which ? a.heads : 0);
+  p.head = j / L;
   return token < a.tokens;
 }
 
-// The place's row of the cache: after the source's load, which does not wait for
+// The place's row of the caches: after the sources' loads, which do not wait for
 // the slot's.
 __device__ __forceinline__ void find_row(const KvArgs& a, Place& p) {
   const int slot = a.slots[p.token];
@@ -53,8 +53,8 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kOther, 0xF, 0xF, true));
 }
 
-__device__ __forceinline__ const uint16_t* source(const KvArgs& a, const Place& p) {
-  return a.src[p.which] + p.token * a.token_stride[p.which] + p.head * a.head_stride[p.which];
+__device__ __forceinline__ const uint16_t* source(const KvArgs& a, const Place& p, int w) {
+  return a.src[w] + p.token * a.token_stride[w] + p.head * a.head_stride[w];
 }
 
 __device__ __forceinline__ void to_floats(u32x4 v, float (&f)[8]) {
@@ -65,10 +65,9 @@ __device__ __forceinline__ void to_floats(u32x4 v, float (&f)[8]) {
   }
 }
 
-// Eight values of a row into the cache in 8 or 4 bits.
+// Eight values of a row into cache w in 8 or 4 bits.
 template <int D, int BITS>
-__device__ __forceinline__ void put(const KvArgs& a, const Place& p, float (&f)[8]) {
-  const int w = p.which;
+__device__ __forceinline__ void put(const KvArgs& a, const Place& p, int w, float (&f)[8]) {
   if constexpr (BITS == 8) {
     float m = 0.f;
 #pragma unroll
@@ -101,20 +100,30 @@ __device__ __forceinline__ void put(const KvArgs& a, const Place& p, float (&f)[
   }
 }
 
+template <int D>
+__device__ __forceinline__ void put16(const KvArgs& a, const Place& p, int w, u32x4 v) {
+  *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.cache[w]) + p.row * D + p.piece * 8) = v;
+}
+
 template <int D, int BITS>
 __global__ __launch_bounds__(256) void kv_write_kernel(const KvArgs a) {
   Place p;
   if (!place<D>(a, (int)(blockIdx.x * 256 + threadIdx.x), p)) return;
-  const u32x4 v = *reinterpret_cast<const u32x4_any*>(source(a, p) + p.piece * 8);
+  u32x4 v[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    v[w] = *reinterpret_cast<const u32x4_any*>(source(a, p, w) + p.piece * 8);
   find_row(a, p);
   if (p.row < 0) return;   // whole rows leave together
-  if constexpr (BITS == 16) {
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.cache[p.which]) + p.row * D + p.piece * 8) =
-        v;
-  } else {
-    float f[8];
-    to_floats(v, f);
-    put<D, BITS>(a, p, f);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    if constexpr (BITS == 16) {
+      put16<D>(a, p, w, v[w]);
+    } else {
+      float f[8];
+      to_floats(v[w], f);
+      put<D, BITS>(a, p, w, f);
+    }
   }
 }
 
@@ -123,26 +132,31 @@ __global__ __launch_bounds__(256) void kv_read_kernel(const KvArgs a) {
   Place p;
   if (!place<D>(a, (int)(blockIdx.x * 256 + threadIdx.x), p)) return;
   find_row(a, p);
-  const int w = p.which;
-  u32x4 v = {0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};  // no such slot: NaN
-  if (p.row >= 0) {
-    if constexpr (BITS == 8) {
-      const u32x2 c = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.cache[w]) +
-                                                      p.row * D + p.piece * 8);
-      const float s = __uint_as_float((uint32_t)a.scale[w][p.row] << 23);
-      v = u32x4{bf16x2_of_e4m3<false>(c[0], s), bf16x2_of_e4m3<true>(c[0], s),
-                bf16x2_of_e4m3<false>(c[1], s), bf16x2_of_e4m3<true>(c[1], s)};
-    } else if constexpr (BITS == 4) {
-      const uint32_t c = *reinterpret_cast<const uint32_t*>(
-          static_cast<const uint8_t*>(a.cache[w]) + p.row * (D / 2) + p.piece * 4);
-      const uint32_t sb = a.scale[w][p.row * (D / kGroup4) + p.piece / (kGroup4 / 8)];
-      v = bf16x8_of_e2m1(c, __uint_as_float(sb << 23));
-    } else {
-      v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.cache[w]) + p.row * D +
-                                          p.piece * 8);
+  u32x4 v[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) v[w] = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+  if (p.row >= 0) {   // else there is no such slot: NaN
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint8_t* rows = static_cast<const uint8_t*>(a.cache[w]);
+      if constexpr (BITS == 8) {
+        const u32x2 c = *reinterpret_cast<const u32x2*>(rows + p.row * D + p.piece * 8);
+        const float s = __uint_as_float((uint32_t)a.scale[w][p.row] << 23);
+        v[w] = u32x4{bf16x2_of_e4m3<false>(c[0], s), bf16x2_of_e4m3<true>(c[0], s),
+                     bf16x2_of_e4m3<false>(c[1], s), bf16x2_of_e4m3<true>(c[1], s)};
+      } else if constexpr (BITS == 4) {
+        const uint32_t c =
+            *reinterpret_cast<const uint32_t*>(rows + p.row * (D / 2) + p.piece * 4);
+        const uint32_t sb = a.scale[w][p.row * (D / kGroup4) + p.piece / (kGroup4 / 8)];
+        v[w] = bf16x8_of_e2m1(c, __uint_as_float(sb << 23));
+      } else {
+        v[w] = *reinterpret_cast<const u32x4*>(rows + (p.row * D + p.piece * 8) * 2);
+      }
     }
   }
-  *reinterpret_cast<u32x4*>(a.dst[w] + (p.token * a.heads + p.head) * D + p.piece * 8) = v;
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    *reinterpret_cast<u32x4*>(a.dst[w] + (p.token * a.heads + p.head) * D + p.piece * 8) = v[w];
 }
 
 // Eight values of a row of k, turned by its token's angles.
@@ -202,20 +216,23 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvArgs a, const Ro
   }
   Place p;
   if (!place<D>(a, (int)((blockIdx.x - q_groups) * 256 + threadIdx.x), p)) return;
-  const uint16_t* row = source(a, p);
-  float f[8];
-  to_floats(*reinterpret_cast<const u32x4_any*>(row + p.piece * 8), f);
-  if (p.which == 0) turn<D, INTERLEAVED>(r, p.token, row, p.piece * 8, f);
+  const uint16_t *k = source(a, p, 0), *v = source(a, p, 1);
+  float f[2][8];
+  to_floats(*reinterpret_cast<const u32x4_any*>(k + p.piece * 8), f[0]);
+  to_floats(*reinterpret_cast<const u32x4_any*>(v + p.piece * 8), f[1]);
+  turn<D, INTERLEAVED>(r, p.token, k, p.piece * 8, f[0]);
   find_row(a, p);
   if (p.row < 0) return;   // whole rows leave together
-  if constexpr (BITS == 16) {
-    u32x4 v;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) v[d] = cvt_pk_bf16(f[2 * d], f[2 * d + 1]);
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.cache[p.which]) + p.row * D + p.piece * 8) =
-        v;
-  } else {
-    put<D, BITS>(a, p, f);
+  for (int w = 0; w < 2; ++w) {
+    if constexpr (BITS == 16) {
+      u32x4 o;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] = cvt_pk_bf16(f[w][2 * d], f[w][2 * d + 1]);
+      put16<D>(a, p, w, o);
+    } else {
+      put<D, BITS>(a, p, w, f[w]);
+    }
   }
 }
 
@@ -223,7 +240,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvArgs a, const Ro
 // 2^30 threads at most.
 template <int D, int BITS, bool WRITE>
 hipError_t run(const KvArgs& a, hipStream_t s) {
-  const int64_t per = (int64_t)2 * a.heads * (D / 8);   // threads of a token
+  const int64_t per = (int64_t)a.heads * (D / 8);   // threads of a token
   const int64_t most = (int64_t(1) << 30) / per;
   for (int64_t at = 0; at < a.tokens; at += most) {
     KvArgs b = a;
@@ -246,7 +263,7 @@ hipError_t run(const KvArgs& a, hipStream_t s) {
 
 template <int D, int BITS>
 hipError_t run_append(const KvArgs& a, RotaryArgs r, hipStream_t s) {
-  const int64_t per = (int64_t)2 * a.heads * (D / 8), per_q = rotary_plan(r);
+  const int64_t per = (int64_t)a.heads * (D / 8), per_q = rotary_plan(r);
   const int64_t most = (int64_t(1) << 30) / (per > per_q ? per : per_q);
   for (int64_t at = 0; at < a.tokens; at += most) {
     KvArgs b = a;
