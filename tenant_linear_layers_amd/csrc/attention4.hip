@@ -99,20 +99,25 @@ __device__ __forceinline__ void read_tr16_4(uint32_t at, u32x4 (&v)[4]) {
 // step's 32 rows are two runs of 16, each contiguous in its page, and a lane's
 // 16 bytes are an operand of K, or a group of V, as they lie there.
 template <int D, int NW>
-__global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnArgs a, const Cut c) {
-  constexpr int R = 16;
-  constexpr int ROWB = D / 2, GROUPS = D / kGroup4;   // bytes, scales of a row
-  constexpr int VLOADS = D / 64;                      // 16 bytes a lane: 32 rows of V
+struct Few4 {
   // V in LDS: rows 32 bytes apart in the banks, so that the eight rows of a
   // transposing read lie in different ones, and every place is a lane's own plus
   // a constant.
-  constexpr int ROWL = 2 * D + 32, STAGE = 32 * ROWL;
-  constexpr int RED = NW * R * (D + 2) * 4;
-  constexpr int SMEM = NW * STAGE > RED ? NW * STAGE : RED;
-  __shared__ __attribute__((aligned(16))) char smem[SMEM];
+  static constexpr int R = 16, ROWL = 2 * D + 32, STAGE = 32 * ROWL;
+  static constexpr int SUMS = NW * R * (D + 2) * 4;
+  static constexpr int SMEM = NW * STAGE > SUMS ? NW * STAGE : SUMS;
+};
+
+template <int D, int NW>
+__device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, int item,
+                                               char* smem) {
+  using F = Few4<D, NW>;
+  constexpr int R = F::R, ROWL = F::ROWL, STAGE = F::STAGE;
+  constexpr int ROWB = D / 2, GROUPS = D / kGroup4;   // bytes, scales of a row
+  constexpr int VLOADS = D / 64;                      // 16 bytes a lane: 32 rows of V
 
   Item it;
-  if (!find_item<false>(a, c, a.first + (int)blockIdx.x, it)) return;
+  if (!find_item<false>(a, c, item, it)) return;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g4 = lane >> 4;
@@ -397,7 +402,8 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&v)[N]) 
 }
 
 template <int D, int RG>
-__global__ __launch_bounds__(256, 2) void attend4_many_kernel(const AttnArgs a, const Cut c) {
+__device__ __forceinline__ void attend4_many(const AttnArgs& a, const Cut& c, int item,
+                                             char* smem) {
   using M = Many4<D, RG>;
   constexpr int KG = M::KG, R = M::R, NB = M::NB, ROW = M::ROW, ROWK = M::ROWK, ROWV = M::ROWV;
   constexpr int AHEAD = M::AHEAD, GROUPS = D / kGroup4;
@@ -408,10 +414,9 @@ __global__ __launch_bounds__(256, 2) void attend4_many_kernel(const AttnArgs a, 
   // Not for tiles of 64 rows of 64 dims (24 mixed sequences 43.4 us, with it 44.1; a
   // prompt of 2048 in tiles of 128 55.5 and 52.1).
   constexpr bool FIRST = D == 128 || RG == 4;
-  __shared__ __attribute__((aligned(16))) char smem[M::SMEM];
 
   Item it;
-  if (!find_item<false>(a, c, a.first + (int)blockIdx.x, it)) return;
+  if (!find_item<false>(a, c, item, it)) return;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rg = wv % RG, kg = wv / RG;
@@ -709,17 +714,49 @@ __global__ __launch_bounds__(256, 2) void attend4_many_kernel(const AttnArgs a, 
   }
 }
 
+// ------------------------------------------------------------------ kernels
+template <int D, int NW>
+__global__ __launch_bounds__(NW * 64, 3) void attend4_rows16_kernel(const AttnArgs a, const Cut c) {
+  __shared__ __attribute__((aligned(16))) char smem[Few4<D, NW>::SMEM];
+  attend4_rows16<D, NW>(a, c, a.first + (int)blockIdx.x, smem);
+}
+
+template <int D, int RG>
+__global__ __launch_bounds__(256, 2) void attend4_many_kernel(const AttnArgs a, const Cut c) {
+  __shared__ __attribute__((aligned(16))) char smem[Many4<D, RG>::SMEM];
+  attend4_many<D, RG>(a, c, a.first + (int)blockIdx.x, smem);
+}
+
+// Both kinds of a call in one launch, the tiles of many rows first: the few
+// rows' items then fill what those leave of the card.
+template <int D, int RG>
+__global__ __launch_bounds__(256, 2) void attend4_both_kernel(AttnArgs a, const Join j) {
+  constexpr int MANY = Many4<D, RG>::SMEM, FEW = Few4<D, 4>::SMEM;
+  __shared__ __attribute__((aligned(16))) char smem[MANY > FEW ? MANY : FEW];
+  const int at = j.first + (int)blockIdx.x, k = at < j.items[1];
+  a.partial = j.partial[k];
+  a.items = j.items[k];
+  if (k) attend4_many<D, RG>(a, j.cut[1], at, smem);
+  else attend4_rows16<D, 4>(a, j.cut[0], at - j.items[1], smem);
+}
+
 template <int D>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
   constexpr int NW = 4;
-  return run_cuts<D>(a, NW * 64, s, [&](const AttnArgs& b, const Cut& c, unsigned grid) {
-    if (c.R == 16)
-      attend4_rows16_kernel<D, NW><<<grid, NW * 64, 0, s>>>(b, c);
-    else if (c.R == 64)
-      attend4_many_kernel<D, 2><<<grid, 256, 0, s>>>(b, c);
-    else
-      attend4_many_kernel<D, 4><<<grid, 256, 0, s>>>(b, c);
-  });
+  return run_cuts<D>(
+      a, NW * 64, s,
+      [&](const AttnArgs& b, const Cut& c, unsigned grid) {
+        if (c.R == 16)
+          attend4_rows16_kernel<D, NW><<<grid, NW * 64, 0, s>>>(b, c);
+        else if (c.R == 64)
+          attend4_many_kernel<D, 2><<<grid, 256, 0, s>>>(b, c);
+        else
+          attend4_many_kernel<D, 4><<<grid, 256, 0, s>>>(b, c);
+      },
+      [&](const AttnArgs& b, const Join& j, unsigned grid) {
+        if (j.cut[1].R == 64) attend4_both_kernel<D, 2><<<grid, 256, 0, s>>>(b, j);
+        else attend4_both_kernel<D, 4><<<grid, 256, 0, s>>>(b, j);
+      });
 }
 
 }  // namespace

@@ -26,6 +26,8 @@
 // and sum of a query are held per lane.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "layer.h"
 
@@ -687,33 +689,48 @@ hipError_t in_parts(int grid, int threads, F launch) {
 }
 
 // A call: the launches of its cuts, then the join of what they cut.
-// launch(b, c, grid) starts `grid` workgroups of cut c, of few_threads threads
-// (R = 16) or 256.
-template <int D, typename F>
-hipError_t run_cuts(AttnArgs a, int few_threads, hipStream_t s, F start) {
+// start(b, c, grid) starts `grid` workgroups of cut c, of few_threads threads
+// (R = 16) or 256.  both(b, j, grid), where there is one, starts those of both
+// cuts, of 256 threads, cut 1's first.
+struct Apart {};   // no `both`
+template <int D, typename F, typename G = Apart>
+hipError_t run_cuts(AttnArgs a, int few_threads, hipStream_t s, F start, G both = G{}) {
   a.by_group = divisor(a.group);
   a.by_page = divisor(a.page);
   a.by_heads = divisor(a.kv_heads);
   const Way w = way_of(a);
   Join j{};
   int joins[2] = {0, 0};
-  for (int k = 1; k >= 0; --k) {
+  for (int k = 0; k < 2; ++k) {
     const Cut& c = w.cut[k];
     if (!c.R) continue;
-    AttnArgs b = a;
-    b.items = w.items[k];
-    b.partial = a.partial + (k ? w.bytes[0] / sizeof(float) : 0);
-    const hipError_t e = in_parts(b.items, c.R == 16 ? few_threads : 256,
-                                  [&](int first, unsigned grid) {
-                                    b.first = first;
-                                    start(b, c, grid);
-                                  });
-    if (e != hipSuccess) return e;
     j.cut[k] = c;
-    j.partial[k] = b.partial;
-    j.items[k] = b.items;
-    if (c.share != 0.f) joins[k] = (b.items - c.target - 8) * (c.R / 16);
+    j.partial[k] = a.partial + (k ? w.bytes[0] / sizeof(float) : 0);
+    j.items[k] = w.items[k];
+    if (c.share != 0.f) joins[k] = (w.items[k] - c.target - 8) * (c.R / 16);
   }
+  hipError_t e = hipSuccess;
+  bool apart = true;
+  if constexpr (!std::is_same_v<G, Apart>) {
+    const int64_t all = (int64_t)j.items[0] + j.items[1];
+    if (j.items[0] && j.items[1] && all <= 2147483647) {
+      apart = false;
+      e = in_parts((int)all, 256, [&](int first, unsigned grid) {
+        j.first = first;
+        both(a, j, grid);
+      });
+    }
+  }
+  for (int k = 1; apart && k >= 0 && e == hipSuccess; --k) {
+    AttnArgs b = a;
+    b.items = j.items[k];
+    b.partial = j.partial[k];
+    e = in_parts(b.items, j.cut[k].R == 16 ? few_threads : 256, [&](int first, unsigned grid) {
+      b.first = first;
+      start(b, j.cut[k], grid);
+    });
+  }
+  if (e != hipSuccess) return e;
   j.from1 = joins[0];
   return in_parts(joins[0] + joins[1], 4 * D, [&](int first, unsigned grid) {
     j.first = first;
