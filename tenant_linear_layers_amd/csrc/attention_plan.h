@@ -579,7 +579,7 @@ int64_t most_tiles(const AttnArgs& a, int R) {
   return all < by_seq ? all : by_seq;
 }
 
-// How a call is carried out: sequences of up to 16 rows on the 16-row kernel,
+// How a call is carried out: sequences of few rows on the 16-row kernel,
 // others on tiles of 64 or 128.  Both kinds in one call are two launches, each
 // with a plan of its own sequences.
 struct Way {
@@ -631,7 +631,7 @@ int rows_a_tile(const AttnArgs& a) {
   return filled && !uneven ? 128 : 64;
 }
 
-Way way_of(const AttnArgs& a) {
+Way way_with(const AttnArgs& a, int few) {   // sequences of up to `few` rows by 16
   Way w{};
   const int64_t rows = (int64_t)a.max_q * a.group;
   const int kAll = 2147483647;
@@ -639,11 +639,11 @@ Way way_of(const AttnArgs& a) {
   // other CUs would save (a token at 4097 keys 14.2 / 14.8 us, in 8 bits 13.7 /
   // 14.5).  1024 of more: 32 sequences in bf16 152 us, 1280 158 us, 1536 155; 40
   // sequences of 8000 keys 231, 245 and 255 (64 in 8 bits 144, 141 and 141).
-  w.cut[0] = Cut{a.group <= 16 ? 16 : 0, 128, 1024, 4, 16, 0, 16, 0.f};
-  if (rows > 16) {
+  w.cut[0] = Cut{a.group <= few ? 16 : 0, 128, 1024, 4, 16, 0, few, 0.f};
+  if (rows > few) {
     w.cut[1] = Cut{rows_a_tile(a), 512, 512, 8, 64, 0, kAll, 0.f};
     if (a.seqs == 1) w.cut[0].R = 0;   // one sequence: one launch, whatever its length
-    if (w.cut[0].R) w.cut[1].least = 16;
+    if (w.cut[0].R) w.cut[1].least = few;
   }
   for (int k = 0; k < 2; ++k) {
     Cut& c = w.cut[k];
@@ -668,11 +668,27 @@ Way way_of(const AttnArgs& a) {
                                     (alike ? c.target : 2 * c.target));
     c.share = may ? (float)a.kv_heads / (float)c.round : 0.f;
     AttnArgs b = a;
-    if (k == 0 && rows > 16) b.max_q = 16 / a.group;
+    if (k == 0 && rows > few) b.max_q = few / a.group;
     w.items[k] = (int)most_items(b, c);
     if (may) w.bytes[k] = (size_t)w.items[k] * c.R * (a.dim + 2) * sizeof(float);
   }
   return w;
+}
+
+// Over 4 bits, where keys are cheap to read again, sequences of up to 32 rows go
+// by 16 too (us so / on tiles of 64 or 128 rows; 8 key/value heads of 128 dims: 4
+// new tokens of 64 heads over 8000 keys 15.3 / 28.9, 16 such sequences over 4000
+// 33.7 / 42.6, 64 over 1000 32.6 / 44.6), and all of a call whose tiles of 16 are
+// less than a workgroup a CU (8 tokens over 8000 17.8 / 31.4, 16 26.6 / 33.2, 4
+// sequences of 8, 128 tiles, 32.8 / 36.2, 1000 from nothing of 2 heads 13.0 / 18.7;
+// but 4 of 16, 256 tiles, 48.6 / 43.7, 8 of 8 46.2 / 44.4, of 64 dims 31.5 / 28.5).
+// Only as far as the workspace goes, whose size does not depend on the cache's
+// type.
+Way way_of(const AttnArgs& a) {
+  const Way w = way_with(a, 16);
+  if (a.bits != 4) return w;
+  const Way f = way_with(a, most_tiles(a, 16) * a.kv_heads <= 192 ? 2147483647 : 32);
+  return f.bytes[0] + f.bytes[1] <= w.bytes[0] + w.bytes[1] ? f : w;
 }
 
 // A launch takes fewer than 2^32 threads: more workgroups than that go in

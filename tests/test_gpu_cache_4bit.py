@@ -216,7 +216,11 @@ def _reference(p, k=None, v=None, **more):
         k, v = _stored(p["cache"])
     ref, mag = OL.paged_attention(_f64(p["q"]), k, v, p["table"].numpy(), p["cu"].tolist(),
                                   p["kv"].tolist(), **more)
-    return ref, 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * mag
+    # A weight below float32's smallest normal number, 2^-126, may be taken for 0: where
+    # the heaviest keys' values are 0, as many of 4 bits are, that is all there is.
+    least = 2.0 ** -126 * p["kv"].max().item() * np.max(np.abs(v), initial=0.0,
+                                                       where=np.isfinite(v))
+    return ref, 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * mag + least
 
 
 def _check(p, out, **more):
