@@ -285,18 +285,21 @@ def rotary_table(frequencies: torch.Tensor, length: int, first: int = 0, magnitu
                  device=None, stream=None) -> torch.Tensor:
     """float32 [length, pairs, 2]: cosine and sine of position * frequency, times
     magnitude, for the positions first .. first + length - 1; angles are taken in
-    64 bits.  frequencies: float64 [pairs], on the host or on the device."""
+    64 bits.  frequencies: float64 [pairs], on a device or on the host, from
+    where they go to `device` (the current one)."""
     if not isinstance(frequencies, torch.Tensor) or frequencies.dtype is not torch.float64 or \
             frequencies.dim() != 1:
         raise TypeError("frequencies must be a float64 tensor [pairs]")
-    if not frequencies.is_cuda:
-        frequencies = frequencies.to("cuda" if device is None else device)
-    dev = _device(frequencies, "frequencies")
+    if frequencies.is_cuda:
+        dev = frequencies.get_device()
+    else:
+        dev = torch.device("cuda" if device is None else device).index
+        dev = _current() if dev is None else dev
     pairs = frequencies.shape[0]
     if length < 0 or first < 0 or pairs < 1:
         raise ValueError("length and first must not be negative, and there must be a pair")
     with _at(dev, stream):
-        frequencies = frequencies.contiguous()
+        frequencies = frequencies.to(f"cuda:{dev}").contiguous()
         table = torch.empty((length, pairs, 2), dtype=torch.float32, device=frequencies.device)
         st = _bd.lib().bitdelta_rotary_table(frequencies.data_ptr(), pairs, first, length,
                                              magnitude, table.data_ptr(), _raw_stream(dev))
