@@ -1,18 +1,29 @@
 // Attention of new tokens over a paged key/value cache in e2m1 with an e8m0
 // scale per 32 dims; the definition and the plan are in attention_plan.h.
 //
-// Scores.  The scaled matrix instructions take K as it is stored: four bits a
-// value, a lane's 16 bytes being one scale's group of a key.  The other operand
+// Scores.  Over few rows, where memory is waited for, a lane converts its part of
+// K in registers (e2m1 times a power of two is a bf16 number) and the products are
+// those of a bf16 cache.
+//
+// Over many rows the scaled matrix instructions take K as it is stored: four bits
+// a value, a lane's 16 bytes being one scale's group of a key.  The other operand
 // is e4m3 at the most precise, four significant bits, so a row of q (bf16,
 // eight) goes in as two, q = hi + lo with the rest of the rounding of the first
 // rounded again (four bits lower): exact for values above 2^-13 of the row's
 // largest, and to 2^-21 of that one below.  Two products at the rate of e4m3 take
-// the time of one in bf16, without a conversion of K.
+// the time of one in bf16, without a conversion of K (which, made once for the
+// workgroup as over 8 bits, is the longest part of a step there).  They add up in
+// float32, but within an instruction a product is kept to about 17 bits below the
+// largest of its 64 (measured on random operands: 5e-6 of the sum on average,
+// 2^-13 of the largest product at most).  The output's error against 64 bits is
+// that of a bf16 cache, of which the weights' rounding is the most: 0.0021 for both,
+// 0.0022 and 0.0018 where one dim's product is 160 for every key, the others'
+// about 2.
 //
 // Values.  The product with V runs over the keys, whose scales differ, so V is
-// converted: e2m1 times a power of two is a bf16 number.  A lane converts 16
-// bytes, one group, by the instruction that takes its scale, writes them to LDS
-// as bf16, and they are read back transposed.
+// converted everywhere.  A lane converts up to 16 bytes of a group by the
+// instruction that takes its scale, writes them to LDS as bf16, and they are read
+// back transposed.
 #include <type_traits>
 
 #include "attention_plan.h"
@@ -25,13 +36,6 @@ namespace bd {
 namespace {
 
 typedef int i32x8 __attribute__((__vector_size__(32)));
-
-// c + a b for 16 keys and queries and 128 dims: a e2m1 (four registers), b e4m3;
-// sa, sb: the scale bytes of the lane's 32 dims of a, of its block of b.
-__device__ __forceinline__ f32x4 mfma16_fp4(u32x4 a, i32x8 b, f32x4 c, uint32_t sa, uint32_t sb) {
-  const i32x8 a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b, c, 4, 0, 0, (int)sa, 0, (int)sb);
-}
 
 // Sixteen values over their row's scale as hi + lo.
 __device__ __forceinline__ void split16(const u32x4 (&v)[2], float is, uint32_t (&hi)[4],
@@ -67,6 +71,26 @@ __device__ __forceinline__ uint32_t magnitude16(const u32x4& v) {
   return m;
 }
 
+// N dwords at an address aligned to all of them.
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&v)[N]) {
+  if constexpr (N == 4) {
+    const u32x4 x = ld128(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = x[i];
+  } else if constexpr (N == 2) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    v[0] = x[0];
+    v[1] = x[1];
+  } else {
+    v[0] = ld32(p);
+  }
+}
+
+__device__ __forceinline__ u32x4 load_past(const uint8_t* p) {   // not to stay in the caches
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+
 // Four blocks of four rows, 32 bytes apart from AT on, and those NEXT bytes
 // behind each; the wait is in the statement.
 template <int AT, int NEXT>
@@ -97,7 +121,14 @@ __device__ __forceinline__ void read_tr16_4(uint32_t at, u32x4 (&v)[4]) {
 // in turn, each with its own stage of V in LDS, so there is no barrier until
 // the waves' sums are joined.  Rows go from memory to registers a step ahead: a
 // step's 32 rows are two runs of 16, each contiguous in its page, and a lane's
-// 16 bytes are an operand of K, or a group of V, as they lie there.
+// bytes are an operand of K, or a group of V, as they lie there.
+//
+// Bound by HBM: 40 sequences of 8000 keys (348 MB) 70 us with their join, 5.0 TB/s
+// (a copy reaches 5.2), 64 of up to 16000 (395 MB) 87 us with it.  A single token at 4097 keys, 8.3 us, is a chain of
+// latencies.  Scaled products, with q split, take as long where the bus is full
+// (70 and 86 us) and longer elsewhere: four new tokens at 8000 keys 15.2 us for
+// 14.4, 64 dims at 64 by 8000 61 for 58.  Three workgroups a CU for 128 dims, 168
+// registers a lane: for four 42 spill.
 template <int D, int NW>
 struct Few4 {
   // V in LDS: rows 32 bytes apart in the banks, so that the eight rows of a
@@ -115,6 +146,7 @@ __device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, 
   constexpr int R = F::R, ROWL = F::ROWL, STAGE = F::STAGE;
   constexpr int ROWB = D / 2, GROUPS = D / kGroup4;   // bytes, scales of a row
   constexpr int VLOADS = D / 64;                      // 16 bytes a lane: 32 rows of V
+  constexpr int KD = D / 4;                           // dims of K a lane and key
 
   Item it;
   if (!find_item<false>(a, c, item, it)) return;
@@ -124,49 +156,16 @@ __device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, 
   const Tile t = tile_of(a, it.q0, it.n, it.len, it.tile, R);
   int lo, hi, kbeg, steps, vis_hi;   // of a pass
 
-  // Q^T: lane (n, g4) has the dims 16 g4 .. + 15 and 64 + 16 g4 .. + 15 of row
-  // n; with 64 dims the second run holds the first one's lower parts, and K's
-  // lanes g4 = 2, 3 the dims of 0, 1 again.
+  // Q^T: lane n's row, the KD dims that the lane's piece of K holds.
   const int my = min(n, t.rows - 1);
   const int qi = a.by_group.of(t.row0 + my);
   const uint16_t* qp =
       a.q + (int64_t)(t.first_q + qi) * a.q_token_stride +
       (int64_t)(it.head * a.group + (t.row0 + my) - qi * a.group) * a.q_head_stride;
-  i32x8 qf[D / 64];
-  uint32_t qs[D / 64];
-  {
-    u32x4 v[D / 64][2];
-    uint32_t m = 0u;
+  u32x4 qf[KD / 8];
 #pragma unroll
-    for (int s = 0; s < D / 64; ++s)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        v[s][e] = *reinterpret_cast<const u32x4_any*>(qp + 64 * s + 16 * g4 + 8 * e);
-        m = max(m, magnitude16(v[s][e]));
-      }
-    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-    const uint32_t sb = query_scale(m);
-    const float is = inv_scale(sb);
-    uint32_t high[D / 64][4], low[D / 64][4];
-#pragma unroll
-    for (int s = 0; s < D / 64; ++s) split16(v[s], is, high[s], low[s]);
-    const uint32_t sl = sb == kNanScale ? sb : sb - 4;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if constexpr (D == 128) {
-        qf[0][w] = (int)high[0][w];
-        qf[0][4 + w] = (int)high[1][w];
-        qf[1][w] = (int)low[0][w];
-        qf[1][4 + w] = (int)low[1][w];
-      } else {
-        qf[0][w] = (int)high[0][w];
-        qf[0][4 + w] = (int)low[0][w];
-      }
-    }
-    qs[0] = D == 128 || g4 < 2 ? sb : sl;
-    if constexpr (D == 128) qs[1] = sl;
-  }
+  for (int s = 0; s < KD / 8; ++s)
+    qf[s] = *reinterpret_cast<const u32x4_any*>(qp + KD * g4 + 8 * s);
   const int pos = t.pos0 + qi;
   const int vis_lo = a.window ? pos - a.window + 1 : 0;
 
@@ -175,8 +174,9 @@ __device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, 
   int blocks = -1;   // lane 2 i + h: rows / 16 of the cache for half h of step i (mod 32)
   const int vpiece = lane % GROUPS;                    // V's group of the lane
   const int vkey = lane / GROUPS;                      // and its row, of the first load
-  // its group of K of 16 rows, and its place among theirs of V
-  const uint32_t koff = n * GROUPS + g4 % GROUPS, voff = lane % (16 * GROUPS);
+  // its bytes of 16 rows of K and of V, and the group of its dims of K
+  const uint32_t koff = n * ROWB + g4 * (KD / 2), voff = lane % (16 * GROUPS) * 16;
+  const int kgroup = g4 * KD / kGroup4;
   char* vput = vst + vkey * ROWL + vpiece * 64;
   const uint32_t vget =
       lds_address(vst + (4 * g4 + (n >> 2)) * ROWL + ((n >> 1) & 1) * 16 + 8 * (n & 1));
@@ -189,7 +189,8 @@ __device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, 
   // own for every operand take 4 us of 80 (40 sequences of 8000 keys).
   const uint8_t* sbase = lane < 32 ? a.scale[0] : a.scale[1];
   struct Rows {
-    u32x4 k[2], v[VLOADS];
+    uint32_t k[2][KD / 8];
+    u32x4 v[VLOADS];
     uint32_t sc;
   };
   auto fetch = [&](int i, Rows& r) {
@@ -212,14 +213,15 @@ __device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, 
     for (int h = 0; h < 2; ++h) {
       blk[h] = max(__builtin_amdgcn_readlane(blocks, 2 * (i & 31) + h), 0);
       const int64_t row = (int64_t)blk[h] * (16 * ROWB);
-      r.k[h] = ld128(a.cache[0] + row + koff * 16);
-      if (D == 128 || lane >= 32 == (h == 1))   // with 64 dims half of the lanes
-        r.v[D == 128 ? h : 0] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4*>(a.cache[1] + row + voff * 16));
+      load_dwords<KD / 8>(a.cache[0] + row + koff, r.k[h]);
+      if (D == 128) r.v[h % VLOADS] = load_past(a.cache[1] + row + voff);
     }
+    if (D == 64)   // a half of the lanes each
+      r.v[0] = load_past(a.cache[1] + (int64_t)(lane < 32 ? blk[0] : blk[1]) * (16 * ROWB) + voff);
     const uint8_t* sp =
         sbase + (int64_t)(lane & 16 ? blk[1] : blk[0]) * (16 * GROUPS) + (lane & 15) * GROUPS;
     r.sc = D == 128 ? ld32(sp) : *reinterpret_cast<const uint16_t*>(sp);
+    __builtin_amdgcn_sched_barrier(0);   // on their way before a step waits for its own
   };
 
   f32x4 acc[D / 16];
@@ -231,7 +233,7 @@ __device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, 
     uint32_t ks[2], vs[VLOADS];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      ks[h] = (uint32_t)__shfl((int)r.sc, 16 * h + n) >> (8 * (g4 % GROUPS));
+      ks[h] = (uint32_t)__shfl((int)r.sc, 16 * h + n) >> (8 * kgroup) & 0xFFu;
 #pragma unroll
     for (int h = 0; h < VLOADS; ++h)
       vs[h] = (uint32_t)__shfl((int)r.sc, 32 + 16 * h + vkey) >> (8 * vpiece) & 0xFFu;
@@ -240,7 +242,8 @@ __device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, 
     for (int h = 0; h < 2; ++h) {
       f32x4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int p = 0; p < D / 64; ++p) z = mfma16_fp4(r.k[h], qf[p], z, ks[h], qs[p]);
+      for (int p = 0; p < KD / 8; ++p)
+        z = mfma16(bf16x8_of_e2m1(r.k[h][p], __uint_as_float(ks[h] << 23)), qf[p], z);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[4 * h + e] = z[e];
     }
@@ -352,6 +355,13 @@ __device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, 
 // wanted one step before V, and their two rings in LDS are NB steps deep each.
 // Rows pass through registers; K is written to LDS as it is, V as bf16, each
 // group times its scale, so that the conversion is made once for the workgroup.
+//
+// A chunk of 509 over 16384 keys (64 heads of 128) takes 257 to 278 us with its
+// join by card, 1000 to 1080 TFLOP/s (a library product 1324; over 8 bits 294), a
+// prompt of 2048 84 us.  The matrix cores are busy 45% of the time, the vector ALU
+// 42% (98 instructions a step beside 12 products, 32 of them the exponentials and
+// their arguments): with two waves a SIMD, as many as 222 registers allow, there
+// is little of either left.
 template <int D, int RG>
 struct Many4 {
   static constexpr int KG = 4 / RG, R = 32 * RG;
@@ -379,28 +389,13 @@ __device__ __forceinline__ f32x16 mfma32_fp4(u32x4 a, i32x8 b, f32x16 c, uint32_
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b, c, 4, 0, P, (int)sa, 0, (int)sb);
 }
 
-// N dwords at an address aligned to all of them, and to one in LDS.
+// N dwords to a place in LDS aligned to all of them.
 template <int N>
 __device__ __forceinline__ void store_dwords(char* p, const uint32_t (&v)[N]) {
   if constexpr (N == 4) *reinterpret_cast<u32x4*>(p) = u32x4{v[0], v[1], v[2], v[3]};
   else if constexpr (N == 2) *reinterpret_cast<u32x2*>(p) = u32x2{v[0], v[1]};
   else *reinterpret_cast<uint32_t*>(p) = v[0];
 }
-template <int N>
-__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&v)[N]) {
-  if constexpr (N == 4) {
-    const u32x4 x = ld128(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = x[i];
-  } else if constexpr (N == 2) {
-    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
-    v[0] = x[0];
-    v[1] = x[1];
-  } else {
-    v[0] = ld32(p);
-  }
-}
-
 template <int D, int RG>
 __device__ __forceinline__ void attend4_many(const AttnArgs& a, const Cut& c, int item,
                                              char* smem) {

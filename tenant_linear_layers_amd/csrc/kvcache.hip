@@ -3,11 +3,14 @@
 //
 // The kernels move each row once and are bound by HBM (2 bytes a value on the
 // bf16 side, 2, 1 + 1/dim or 1/2 + 1/32 on the cache's) or, for a batch of
-// single tokens, by the launch.  dim / 8 neighbouring lanes hold a row: one
-// 16-byte access a lane on the bf16 side, and a group's largest magnitude by
-// lane exchanges, so a row needs no LDS.  Neighbouring rows of a token are its
-// heads, contiguous on the side of the tokens.  64 tokens into 8 bits take 3.3
-// us, 2048 5.9 us, 16001 back 20.6 us (4.8 TB/s; a copy reaches 4.9).
+// single tokens, by the launch.  dim / 8 neighbouring lanes hold a row of k and
+// of v: one 16-byte access a lane and row on the bf16 side, and a group's largest
+// magnitude by lane exchanges, so a row needs no LDS.  Neighbouring rows of a
+// token are its heads, contiguous on the side of the tokens.  8 heads of 128: 64
+// tokens into 8 or 4 bits take 2.6 us, 2048 4.4 and 4.1, 16001 19.6 and 19.0, back
+// 17.3 and 19.0 (4 bits, from cold memory and single slots: 22.8 and 20.7, 3.6 and
+// 4.0 TB/s of what is needed; a slot's 4 bytes of scales move 32 and its 64 of
+// codes half a line).
 #include "common.h"
 #include "e2m1.h"
 #include "e4m3.h"

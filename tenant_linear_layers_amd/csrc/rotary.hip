@@ -1,8 +1,9 @@
 // Rotary positions: rows of bf16 heads turned by the angles of their tokens'
 // positions, and the table of cosines and sines that the angles come from.
 //
-// A rotation reads and writes 2 bytes a value and is bound by HBM, or, for few
-// tokens, by the launch.  The cosines and sines (float32, 4 bytes a value) are
+// A rotation reads and writes 2 bytes a value and is bound by HBM (16001 tokens of
+// 64 heads of 128 102 us, 5.1 TB/s, as a copy; 2048 12.1 us), or, for few tokens,
+// by the launch (2.4 us).  The cosines and sines (float32, 4 bytes a value) are
 // read from a table rather than computed: a far position times a frequency
 // needs 64 bits to keep the angle's fraction of a turn.
 #include "rotary.h"
