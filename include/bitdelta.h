@@ -519,7 +519,8 @@ int bitdelta_rotary(const uint16_t* x, int64_t x_token_stride, int64_t x_head_st
  * within -120..120 (-120 for a group of zeros); magnitudes above 6 * 2^120
  * (infinities among them) are held to it.  e2m1 has no NaN: a group that holds
  * one gets the scale byte 255, e8m0's NaN, and all of it is NaN.  In a cache
- * filled by other means every byte is read as e8m0 says.
+ * filled by other means a scale is read as e8m0 says; with bytes 253 and 254 the
+ * larger values of a group are past bf16's range.
  *
  * bitdelta_kv_write puts row t of k and v into slot slots[t]; a slot outside
  * the cache (a negative one for padding) is passed over.  The slots of a call
