@@ -638,8 +638,13 @@ Way way_with(const AttnArgs& a, int few) {   // sequences of up to `few` rows by
   // 128 pieces of little work, not one a CU: their join is longer than what the
   // other CUs would save (a token at 4097 keys 14.2 / 14.8 us, in 8 bits 13.7 /
   // 14.5).  1024 of more: 32 sequences in bf16 152 us, 1280 158 us, 1536 155; 40
-  // sequences of 8000 keys 231, 245 and 255 (64 in 8 bits 144, 141 and 141).
-  w.cut[0] = Cut{a.group <= few ? 16 : 0, 128, 1024, 4, 16, 0, few, 0.f};
+  // sequences of 8000 keys 231, 245 and 255 (64 in 8 bits 144, 141 and 141).  768
+  // over 4 bits of 128 dims, the three workgroups of a CU (with 1024 / 768: 32
+  // sequences of 8000 keys 60.6 / 57.3, 10 of 16000 46.5 / 43.1, 24 of up to 16000
+  // 47.2 / 45.3, 64 88 / 88, 16 tokens over 8000 25.5 / 22.1; but where that leaves
+  // a short second round 20 sequences of 12000 56.9 / 62.2, 40 of 8000 69.6 / 72.5).
+  const int target = a.bits == 4 && a.dim == 128 ? 768 : 1024;
+  w.cut[0] = Cut{a.group <= few ? 16 : 0, 128, target, 4, 16, 0, few, 0.f};
   if (rows > few) {
     w.cut[1] = Cut{rows_a_tile(a), 512, 512, 8, 64, 0, kAll, 0.f};
     if (a.seqs == 1) w.cut[0].R = 0;   // one sequence: one launch, whatever its length
@@ -677,11 +682,11 @@ Way way_with(const AttnArgs& a, int few) {   // sequences of up to `few` rows by
 
 // Over 4 bits, where keys are cheap to read again, sequences of up to 32 rows go
 // by 16 too (us so / on tiles of 64 or 128 rows; 8 key/value heads of 128 dims: 4
-// new tokens of 64 heads over 8000 keys 15.3 / 28.9, 16 such sequences over 4000
-// 33.7 / 42.6, 64 over 1000 32.6 / 44.6), and all of a call whose tiles of 16 are
-// less than a workgroup a CU (8 tokens over 8000 17.8 / 31.4, 16 26.6 / 33.2, 4
-// sequences of 8, 128 tiles, 32.8 / 36.2, 1000 from nothing of 2 heads 13.0 / 18.7;
-// but 4 of 16, 256 tiles, 48.6 / 43.7, 8 of 8 46.2 / 44.4, of 64 dims 31.5 / 28.5).
+// new tokens of 64 heads over 8000 keys 14.6 / 28.9, 16 such sequences over 4000
+// 31.4 / 42.6, 64 over 1000 32.6 / 44.6), and all of a call whose tiles of 16 are
+// less than a workgroup a CU (8 tokens over 8000 17.6 / 31.4, 16 22.1 / 33.2, 4
+// sequences of 8, 128 tiles, 29.9 / 36.2, 1000 from nothing of 2 heads 13.0 / 18.7;
+// but 4 of 16, 256 tiles, 43.5 / 40.1, 8 of 8 44.0 / 42.9, of 64 dims 29.7 / 28.5).
 // Only as far as the workspace goes, whose size does not depend on the cache's
 // type.
 Way way_of(const AttnArgs& a) {
