@@ -123,12 +123,12 @@ __device__ __forceinline__ void read_tr16_4(uint32_t at, u32x4 (&v)[4]) {
 // step's 32 rows are two runs of 16, each contiguous in its page, and a lane's
 // bytes are an operand of K, or a group of V, as they lie there.
 //
-// Bound by HBM: 40 sequences of 8000 keys (348 MB) 70 us with their join, 5.0 TB/s
-// (a copy reaches 5.2), 64 of up to 16000 (395 MB) 87 us.  A single token at 4097
-// keys, 8.3 us, is a chain of latencies.  Scaled products, with q split, take as
-// long where the bus is full (70 and 86 us) and longer elsewhere: four new tokens
-// at 8000 keys 15.2 us for 14.4, 64 dims at 64 by 8000 61 for 58.  Three workgroups
-// a CU for 128 dims, 168 registers a lane: for four 42 spill.
+// Bound by HBM: 32 sequences of 8000 keys (279 MB) 57 us with their join, 4.9 TB/s
+// (a copy reaches 5.2), 64 of up to 16000 (395 MB) 82 to 88 by card.  A single token
+// at 4097 keys, 8.3 us, is a chain of latencies.  Scaled products, with q split, take
+// as long where the bus is full and longer elsewhere: four new tokens at 8000 keys
+// 15.2 us for 14.4, 64 dims at 64 by 8000 61 for 58.  Three workgroups a CU for 128
+// dims, 168 registers a lane: for four 42 spill.
 template <int D, int NW>
 struct Few4 {
   // V in LDS: rows 32 bytes apart in the banks, so that the eight rows of a
