@@ -616,9 +616,7 @@ int bitdelta_paged_attention(const uint16_t* q, int64_t q_token_stride, int64_t 
                              void* stream);
 
 /* bitdelta_paged_attention_4bit - the same over a 4-bit cache, its scales
- * [pages, kv_heads, page, dim / 32]; the same workspace.  For sequences of many rows
- * a score's products are kept to about 17 bits below the largest of them before
- * they are added in float32, and q to 2^-21 of its row's largest value. */
+ * [pages, kv_heads, page, dim / 32]; the same workspace. */
 int bitdelta_paged_attention_4bit(
     const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
     const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* table,

@@ -1,24 +1,15 @@
 // Attention of new tokens over a paged key/value cache in e2m1 with an e8m0
 // scale per 32 dims; the definition and the plan are in attention_plan.h.
 //
-// Scores.  Over few rows, where memory is waited for, a lane converts its part of
-// K in registers (e2m1 times a power of two is a bf16 number) and the products are
-// those of a bf16 cache.
-//
-// Over many rows the scaled matrix instructions take K as it is stored: four bits
-// a value, a lane's 16 bytes being one scale's group of a key.  The other operand
-// is e4m3 at the most precise, four significant bits, so a row of q (bf16,
-// eight) goes in as two, q = hi + lo with the rest of the rounding of the first
-// rounded again (four bits lower): exact for values above 2^-13 of the row's
-// largest, and to 2^-21 of that one below.  Two products at the rate of e4m3 take
-// the time of one in bf16, without a conversion of K (which, made once for the
-// workgroup as over 8 bits, is the longest part of a step there).  They add up in
-// float32, but within an instruction a product is kept to about 17 bits below the
-// largest of its 64 (measured on random operands: 5e-6 of the sum on average,
-// 2^-13 of the largest product at most).  The output's error against 64 bits is
-// that of a bf16 cache, of which the weights' rounding is the most: 0.0021 for both,
-// 0.0022 and 0.0018 where one dim's product is 160 for every key, the others'
-// about 2.
+// Scores.  A lane converts its part of K in registers (e2m1 times a power of two is
+// a bf16 number), and the products are those of a bf16 cache, exact and summed in
+// float32.  Over many rows the scaled matrix instructions would take K as it is
+// stored, with a row of q as two parts of e4m3, in the same time on the matrix cores
+// and without the conversion, 32 vector instructions a step and wave (a chunk of 509
+// over 16384 keys 266 us for 293, a prompt of 2048 85 for 89, mixed calls 0 to 5%
+// less).  But they keep a product to about 17 bits below the largest of its group: with
+// one dim of q at 512 or 1024 against keys of 4 the output's error was 0.012 to 0.017
+// and 0.030 to 0.043, so 0.0018, the roundings' own.
 //
 // Values.  The product with V runs over the keys, whose scales differ, so V is
 // converted everywhere.  A lane converts up to 16 bytes of a group by the
@@ -34,42 +25,6 @@
 
 namespace bd {
 namespace {
-
-typedef int i32x8 __attribute__((__vector_size__(32)));
-
-// Sixteen values over their row's scale as hi + lo.
-__device__ __forceinline__ void split16(const u32x4 (&v)[2], float is, uint32_t (&hi)[4],
-                                        uint32_t (&lo)[4]) {
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    float x[4], r[4];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t two = v[w >> 1][2 * (w & 1) + e];
-      x[2 * e] = lo16(two) * is;
-      x[2 * e + 1] = hi16(two) * is;
-    }
-    hi[w] = pack_e4m3(x[0], x[1], x[2], x[3]);
-    r[0] = x[0] - __builtin_amdgcn_cvt_f32_fp8((int)hi[w], 0);
-    r[1] = x[1] - __builtin_amdgcn_cvt_f32_fp8((int)hi[w], 1);
-    r[2] = x[2] - __builtin_amdgcn_cvt_f32_fp8((int)hi[w], 2);
-    r[3] = x[3] - __builtin_amdgcn_cvt_f32_fp8((int)hi[w], 3);
-    lo[w] = pack_e4m3(r[0] * 16.f, r[1] * 16.f, r[2] * 16.f, r[3] * 16.f);
-  }
-}
-
-// The scale byte of a row of q by its largest magnitude's bits; a row with a
-// NaN or an infinity is NaN as a whole, as are its scores.
-__device__ __forceinline__ uint32_t query_scale(uint32_t bits) {
-  return bits >= 0x7F800000u ? kNanScale : scale_byte(__uint_as_float(bits));
-}
-
-__device__ __forceinline__ uint32_t magnitude16(const u32x4& v) {
-  uint32_t m = 0u;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) m = max(m, max((v[d] << 16) & 0x7FFF0000u, v[d] & 0x7FFF0000u));
-  return m;
-}
 
 // N dwords at an address aligned to all of them.
 template <int N>
@@ -353,15 +308,16 @@ __device__ __forceinline__ void attend4_rows16(const AttnArgs& a, const Cut& c, 
 // The products for the scores of step i + 1 come before the softmax of step i,
 // so that the matrix cores work while rows are staged and maxima taken: K is
 // wanted one step before V, and their two rings in LDS are NB steps deep each.
-// Rows pass through registers; K is written to LDS as it is, V as bf16, each
-// group times its scale, so that the conversion is made once for the workgroup.
+// Rows pass through registers; K is written to LDS as it is and converted by each
+// wave for its products (as bf16 it would be four times the reads of LDS), V as bf16,
+// each group times its scale, so that the conversion is made once for the workgroup.
 //
-// A chunk of 509 over 16384 keys (64 heads of 128) takes 257 to 278 us with its
-// join by card, 1000 to 1080 TFLOP/s (a library product 1324; over 8 bits 294), a
-// prompt of 2048 84 us.  The matrix cores are busy 45% of the time, the vector ALU
-// 42% (98 instructions a step beside 12 products, 32 of them the exponentials and
-// their arguments): with two waves a SIMD, as many as 222 registers allow, there
-// is little of either left.
+// A chunk of 509 over 16384 keys (64 heads of 128) takes 291 to 293 us with its
+// join, 950 TFLOP/s (a library product 1324; over 8 bits 300), a prompt of 2048 88
+// to 95 us by card.  The matrix cores are busy 41% of the time, the vector ALU 49%
+// (168 instructions a step beside 16 products, 32 of them K's conversion, 32 the
+// exponentials and their arguments): with two waves a SIMD, as many as 226 registers
+// allow, there is little of either left.
 template <int D, int RG>
 struct Many4 {
   static constexpr int KG = 4 / RG, R = 32 * RG;
@@ -379,15 +335,6 @@ struct Many4 {
 
 template <int I>
 using Step = std::integral_constant<int, I>;
-
-// c + a b for 32 keys and queries and 64 dims; byte P of sa is the scale of the
-// lane's 32 dims of a.
-template <int P>
-__device__ __forceinline__ f32x16 mfma32_fp4(u32x4 a, i32x8 b, f32x16 c, uint32_t sa,
-                                             uint32_t sb) {
-  const i32x8 a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b, c, 4, 0, P, (int)sa, 0, (int)sb);
-}
 
 // N dwords to a place in LDS aligned to all of them.
 template <int N>
@@ -425,33 +372,10 @@ __device__ __forceinline__ void attend4_many(const AttnArgs& a, const Cut& c, in
   const int qi = a.by_group.of(my);
   const uint16_t* qp = a.q + (int64_t)(t.first_q + qi) * a.q_token_stride +
                        (int64_t)(it.head * a.group + my - qi * a.group) * a.q_head_stride;
-  i32x8 qh[D / 64], ql[D / 64];
-  uint32_t qsh, qsl;
-  {
-    u32x4 v[D / 32][2];
-    uint32_t m = 0u;
+  u32x4 qf[D / 16];
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        v[s][e] = *reinterpret_cast<const u32x4_any*>(qp + 32 * s + 16 * hh + 8 * e);
-        m = max(m, magnitude16(v[s][e]));
-      }
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-    qsh = query_scale(m);
-    qsl = qsh == kNanScale ? qsh : qsh - 4;
-    const float is = inv_scale(qsh);
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-      uint32_t high[4], low[4];
-      split16(v[s], is, high, low);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        qh[s >> 1][4 * (s & 1) + w] = (int)high[w];
-        ql[s >> 1][4 * (s & 1) + w] = (int)low[w];
-      }
-    }
-  }
+  for (int e = 0; e < D / 16; ++e)
+    qf[e] = *reinterpret_cast<const u32x4_any*>(qp + 64 * (e >> 2) + 32 * hh + 8 * (e & 3));
   const int vis_lo = a.window ? t.pos0 + qi - a.window + 1 : 0;
   // the first and last query of the wave's rows: keys that all of them see
   const int first_q = a.by_group.of(t.row0 + min(32 * rg, t.rows - 1));
@@ -545,10 +469,13 @@ __device__ __forceinline__ void attend4_many(const AttnArgs& a, const Cut& c, in
     return *reinterpret_cast<const u32x4*>(kring + at * M::STAGEK + n * ROWK + 16 * hh + 32 * p);
   };
   auto scores = [&](const u32x4 (&kf)[D / 64], uint32_t ks) {
-    f32x16 z = mfma32_fp4<0>(kf[0], qh[0], nil, ks, qsh);
-    if constexpr (D == 128) z = mfma32_fp4<2>(kf[1], qh[1], z, ks, qsh);
-    z = mfma32_fp4<0>(kf[0], ql[0], z, ks, qsl);
-    if constexpr (D == 128) z = mfma32_fp4<2>(kf[1], ql[1], z, ks, qsl);
+    f32x16 z = nil;
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p) {
+      const float sc = __uint_as_float((ks >> (16 * p) & 0xFFu) << 23);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z = mfma32(bf16x8_of_e2m1(kf[p][e], sc), qf[4 * p + e], z);
+    }
     return z;
   };
 
