@@ -667,8 +667,7 @@ Divisor divisor(int by) {
 }
 
 size_t paged_attention_workspace(const AttnArgs& a) {
-  const Way w = way_of(a);
-  return w.bytes[0] + w.bytes[1];
+  return way_bytes(way_of_size(a));
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t s) {

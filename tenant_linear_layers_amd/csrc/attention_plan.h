@@ -580,8 +580,8 @@ int64_t most_tiles(const AttnArgs& a, int R) {
 }
 
 // How a call is carried out: sequences of few rows on the 16-row kernel,
-// others on tiles of 64 or 128.  Both kinds in one call are two launches, each
-// with a plan of its own sequences.
+// others on tiles of 64 or 128.  Both kinds in one call have each a plan of its own
+// sequences, in two launches or, over 4 bits, in one.
 struct Way {
   Cut cut[2];        // few rows, many rows; R = 0: no such sequences
   int items[2];      // grids
@@ -680,6 +680,16 @@ Way way_with(const AttnArgs& a, int few) {   // sequences of up to `few` rows by
   return w;
 }
 
+// Bytes of a plan's sums.
+size_t way_bytes(const Way& w) { return w.bytes[0] + w.bytes[1]; }
+
+// The plan of bf16 and e4m3 caches, and what the workspace is sized by for every
+// type: a caller asks for the size without naming one.
+Way way_of_size(AttnArgs a) {
+  a.bits = 16;
+  return way_with(a, 16);
+}
+
 // Over 4 bits, where keys are cheap to read again, sequences of up to 32 rows go
 // by 16 too (us so / on tiles of 64 or 128 rows; 8 key/value heads of 128 dims: 4
 // new tokens of 64 heads over 8000 keys 14.6 / 28.9, 16 such sequences over 4000
@@ -687,13 +697,17 @@ Way way_with(const AttnArgs& a, int few) {   // sequences of up to `few` rows by
 // less than a workgroup a CU (8 tokens over 8000 17.6 / 31.4, 16 22.1 / 33.2, 4
 // sequences of 8, 128 tiles, 29.9 / 36.2, 1000 from nothing of 2 heads 13.0 / 18.7;
 // but 4 of 16, 256 tiles, 43.5 / 40.1, 8 of 8 44.0 / 42.9, of 64 dims 29.7 / 28.5).
-// Only as far as the workspace goes, whose size does not depend on the cache's
-// type.
+// A plan is taken only where it fits into the workspace that way_of_size asks for
+// (with very many sequences, such as 100 of 4 tokens with one of 100, the one by 32
+// does not); way_of_size itself is the last, so no target above has to be below another.
 Way way_of(const AttnArgs& a) {
-  const Way w = way_with(a, 16);
-  if (a.bits != 4) return w;
-  const Way f = way_with(a, most_tiles(a, 16) * a.kv_heads <= 192 ? 2147483647 : 32);
-  return f.bytes[0] + f.bytes[1] <= w.bytes[0] + w.bytes[1] ? f : w;
+  const Way all = way_of_size(a);
+  if (a.bits != 4) return all;
+  for (int few : {most_tiles(a, 16) * a.kv_heads <= 192 ? 2147483647 : 32, 16}) {
+    const Way w = way_with(a, few);
+    if (way_bytes(w) <= way_bytes(all)) return w;
+  }
+  return all;
 }
 
 // A launch takes fewer than 2^32 threads: more workgroups than that go in
