@@ -648,7 +648,15 @@ Way way_with(const AttnArgs& a, int few) {   // sequences of up to `few` rows by
   if (rows > few) {
     w.cut[1] = Cut{rows_a_tile(a), 512, 512, 8, 64, 0, kAll, 0.f};
     if (a.seqs == 1) w.cut[0].R = 0;   // one sequence: one launch, whatever its length
-    if (w.cut[0].R) w.cut[1].least = few;
+    if (w.cut[0].R) {
+      w.cut[1].least = few;
+      // The kernel of both kinds has the registers of its tiles of many rows: over 4
+      // bits two workgroups of 128 dims a CU, three of 64.  60 single tokens and 4 of
+      // 20 over 4000 keys with 768 / 512 98.5 / 92 us, 60 and one of 20 80.5 / 74, 200
+      // tokens over 4000 with 40 single ones over 8000 124 / 126; of 64 dims, with 1024
+      // / 768, 200 with 40 75 / 72, 24 mixed ones 37.2 / 36.4, others alike.
+      if (a.bits == 4) w.cut[0].target = a.dim == 128 ? 512 : 768;
+    }
   }
   for (int k = 0; k < 2; ++k) {
     Cut& c = w.cut[k];
@@ -697,6 +705,9 @@ Way way_of_size(AttnArgs a) {
 // less than a workgroup a CU (8 tokens over 8000 17.6 / 31.4, 16 22.1 / 33.2, 4
 // sequences of 8, 128 tiles, 29.9 / 36.2, 1000 from nothing of 2 heads 13.0 / 18.7;
 // but 4 of 16, 256 tiles, 43.5 / 40.1, 8 of 8 44.0 / 42.9, of 64 dims 29.7 / 28.5).
+// Beside longer ones too: 20 single tokens, 20 of 4 and one of 100 over 4000 keys 86 /
+// 97, 32 of 3 with one of 64 over 2000 52 / 61, 16 of 4 with one of 200 over 4000 83 /
+// 87.5, of 64 dims 49 / 62.
 // A plan is taken only where it fits into the workspace that way_of_size asks for
 // (with very many sequences, such as 100 of 4 tokens with one of 100, the one by 32
 // does not); way_of_size itself is the last, so no target above has to be below another.

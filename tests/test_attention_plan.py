@@ -48,6 +48,42 @@ def plan(tmp_path_factory):
     return run
 
 
+def _call(new, kv, heads, kv_heads, dim, page, bits=4):
+    width = max(-(-m // page) for m in kv)
+    return (sum(new), len(new), max(new), heads, kv_heads, dim, width, page, bits)
+
+
+ALL = 2 ** 31 - 1
+WAYS = [
+    # new, kv, heads, kv_heads, dim, most rows of a sequence by 16, rows of the others' tiles
+    ([1] * 40, [8000] * 40, 64, 8, 128, 32, 0),
+    ([4] * 16, [4000] * 16, 64, 8, 128, 32, 0),
+    ([4] * 16 + [200], [4000] * 17, 64, 8, 128, 32, 128),
+    ([4] * 16 + [200], [4000] * 17, 64, 8, 64, 32, 128),
+    ([4] * 40 + [100], [8000] * 41, 64, 8, 128, 32, 64),
+    ([2] * 20 + [4] * 20 + [100], [4000] * 41, 64, 8, 128, 32, 64),
+    ([3, 100, 4, 1], [900, 2000, 700, 5000], 64, 8, 64, 32, 128),
+    ([4] * 100 + [100], [1000] * 101, 64, 8, 128, 16, 64),   # by 32 it would not fit
+    ([1, 40], [150, 90], 8, 8, 128, ALL, 0),                 # 32 tiles in all
+    ([20, 20], [200, 200], 8, 2, 128, ALL, 0),
+    ([16], [8000], 64, 8, 128, ALL, 0),
+    ([40], [90], 64, 64, 128, 0, 64),
+    ([2048], [2048], 64, 8, 128, 0, 128),
+    ([70, 40], [70, 300], 64, 64, 128, 32, 64),
+    ([200], [500], 64, 16, 64, 0, 128),
+]
+
+
+@pytest.mark.parametrize("new,kv,heads,kv_heads,dim,by16,rows", WAYS)
+def test_which_rows_go_by_16(plan, new, kv, heads, kv_heads, dim, by16, rows):
+    w, = plan([_call(new, kv, heads, kv_heads, dim, 64)])
+    assert w["few"] == (16 if by16 else 0) and w["many"] == rows
+    if by16:
+        assert w["most"] == by16
+    if by16 and rows:
+        assert w["least"] == by16
+
+
 def test_no_plan_needs_more_than_the_size_asked_for(plan):
     """Whatever the cache's type is, which the size query does not know."""
     rng = random.Random(4)
