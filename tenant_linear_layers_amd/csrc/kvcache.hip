@@ -7,7 +7,7 @@
 // of v: one 16-byte access a lane and row on the bf16 side, and a group's largest
 // magnitude by lane exchanges, so a row needs no LDS.  Neighbouring rows of a
 // token are its heads, contiguous on the side of the tokens.  8 heads of 128: 64
-// tokens into 8 or 4 bits take 2.6 us, 2048 4.4 and 4.1, 16001 19.6 and 19.0, back
+// tokens into 8 or 4 bits take 3.2 and 3.0 us, 2048 4.4 and 4.1, 16001 19.6 and 18.8, back
 // 17.3 and 19.0 (4 bits, from cold memory and single slots: 22.8 and 20.7, 3.6 and
 // 4.0 TB/s of what is needed; a slot's 4 bytes of scales move 32 and its 64 of
 // codes half a line).
@@ -38,8 +38,11 @@ __device__ __forceinline__ bool place(const KvArgs& a, int i, Place& p) {
   return token < a.tokens;
 }
 
-// The place's row of the caches: after the sources' loads, which do not wait for
-// the slot's.
+// The place's row of the caches.  Writes look it up before they read a token, so one
+// that is passed over costs its slot's four bytes: of 16001 tokens, half of them
+// padding, a write takes 12 us, with the rows read beside the slots 16 to 17, and an
+// append (64 heads and 8) 115 to 119 for 121 to 125.  Without padding that is up to
+// 0.1 us of 3 for few tokens, and nothing or up to 1% for many.
 __device__ __forceinline__ void find_row(const KvArgs& a, Place& p) {
   const int slot = a.slots[p.token];
   const int page = a.by_page.of(max(slot, 0));
@@ -112,12 +115,12 @@ template <int D, int BITS>
 __global__ __launch_bounds__(256) void kv_write_kernel(const KvArgs a) {
   Place p;
   if (!place<D>(a, (int)(blockIdx.x * 256 + threadIdx.x), p)) return;
+  find_row(a, p);
+  if (p.row < 0) return;   // whole rows leave together
   u32x4 v[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w)
     v[w] = *reinterpret_cast<const u32x4_any*>(source(a, p, w) + p.piece * 8);
-  find_row(a, p);
-  if (p.row < 0) return;   // whole rows leave together
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     if constexpr (BITS == 16) {
@@ -219,13 +222,13 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvArgs a, const Ro
   }
   Place p;
   if (!place<D>(a, (int)((blockIdx.x - q_groups) * 256 + threadIdx.x), p)) return;
+  find_row(a, p);
+  if (p.row < 0) return;   // whole rows leave together
   const uint16_t *k = source(a, p, 0), *v = source(a, p, 1);
   float f[2][8];
   to_floats(*reinterpret_cast<const u32x4_any*>(k + p.piece * 8), f[0]);
   to_floats(*reinterpret_cast<const u32x4_any*>(v + p.piece * 8), f[1]);
   turn<D, INTERLEAVED>(r, p.token, k, p.piece * 8, f[0]);
-  find_row(a, p);
-  if (p.row < 0) return;   // whole rows leave together
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     if constexpr (BITS == 16) {
