@@ -71,6 +71,8 @@ WAYS = [
     ([2048], [2048], 64, 8, 128, 0, 128),
     ([70, 40], [70, 300], 64, 64, 128, 32, 64),
     ([200], [500], 64, 16, 64, 0, 128),
+    ([40, 70], [90, 150], 64, 64, 128, 32, 64),
+    ([200], [500], 64, 16, 128, 0, 128),
 ]
 
 
