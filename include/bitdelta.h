@@ -587,6 +587,8 @@ int bitdelta_kv_append(const uint16_t* q, int64_t q_token_stride, int64_t q_head
  * no key is zero.  NaN and infinities in the cache or in q reach the rows that
  * see them only.  Scores, maxima and sums are float32; the probabilities
  * are rounded to bf16 for the product with v, and add up to one as rounded.
+ * Values are summed with weights of up to 2^6 before the division by their
+ * total: a row may not be finite in dims where such a sum passes 2^128.
  *   q         device, bf16 [tokens, heads, dim], strides in elements
  *   table     device, int32 [seqs, width]; entries of pages that no row sees
  *             are not read.  A page outside [0, pages) that a row sees makes
