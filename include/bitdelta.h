@@ -459,7 +459,9 @@ int bitdelta_rms_norm_mx(const uint16_t* x, int64_t x_stride, const uint16_t* re
  *   h = residual + alpha * gate * u         (gate NULL: 1)
  *   y = h / sqrt(mean(h^2) + eps) * w
  * Everything between the inputs and the roundings of h_out and y to bf16 is
- * float32; the second norm is taken of the unrounded h.
+ * float32; the second norm is taken of the unrounded h.  As in bitdelta_rms_norm a
+ * row whose sum of squares passes 2^128 is zeros after its norm: of x, so that h is
+ * the residual (with post only), and of h, so that y is zeros.
  *   x, residual, gate   device, bf16 [rows, cols], rows x_stride / r_stride /
  *                       g_stride elements apart (0: one row for all)
  *   post, w             device, bf16 [cols]

@@ -200,7 +200,8 @@ def rms_norm_block(x: torch.Tensor, residual: torch.Tensor, post_weight, weight:
         y = h / sqrt(mean(h^2) + eps) * weight
 
     x, residual, y, h: bf16 [..., cols]; gate: bf16 of that shape or [cols];
-    post_weight, weight: bf16 [cols]; scale: finite."""
+    post_weight, weight: bf16 [cols]; scale: finite.  The sums of squares are
+    float32: of a row whose sum passes 2^128 the norm is zeros."""
     gs = 0
     try:
         shape = x.shape
