@@ -287,18 +287,22 @@ def rotary_table(frequencies: torch.Tensor, length: int, first: int = 0, magnitu
     """float32 [length, pairs, 2]: cosine and sine of position * frequency, times
     magnitude, for the positions first .. first + length - 1; angles are taken in
     64 bits.  frequencies: float64 [pairs], on a device or on the host, from
-    where they go to `device` (the current one)."""
+    where they go to `device` (the current one); the table is on that device."""
     if not isinstance(frequencies, torch.Tensor) or frequencies.dtype is not torch.float64 or \
             frequencies.dim() != 1:
         raise TypeError("frequencies must be a float64 tensor [pairs]")
-    if frequencies.is_cuda:
-        dev = frequencies.get_device()
-    else:
-        dev = torch.device("cuda" if device is None else device).index
-        dev = _current() if dev is None else dev
     pairs = frequencies.shape[0]
     if length < 0 or first < 0 or pairs < 1:
         raise ValueError("length and first must not be negative, and there must be a pair")
+    want = torch.device("cuda" if device is None else device)
+    if want.type != "cuda":
+        raise ValueError(f"device must be a HIP device, got {want}")
+    if frequencies.is_cuda:
+        dev = frequencies.get_device()
+        if want.index is not None and want.index != dev:
+            raise ValueError(f"frequencies are on {frequencies.device}, device is {want}")
+    else:
+        dev = _current() if want.index is None else want.index
     with _at(dev, stream):
         frequencies = frequencies.to(f"cuda:{dev}").contiguous()
         table = torch.empty((length, pairs, 2), dtype=torch.float32, device=frequencies.device)
