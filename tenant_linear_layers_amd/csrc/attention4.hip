@@ -79,8 +79,8 @@ __device__ __forceinline__ void read_tr16_4(uint32_t at, u32x4 (&v)[4]) {
 // bytes are an operand of K, or a group of V, as they lie there.
 //
 // Bound by HBM: 32 sequences of 8000 keys (279 MB) 57 us with their join, 4.9 TB/s
-// (a copy reaches 5.2), 64 of up to 16000 (395 MB) 82 to 88 by card.  A single token
-// at 4097 keys, 8.3 us, is a chain of latencies.  Scaled products, with q split, take
+// (a copy reaches 5.2), 64 of 1000 to 16000 (364 to 395 MB as they are drawn) 82 to
+// 91 by card.  A single token at 4097 keys, 8.3 us, is a chain of latencies.  Scaled products, with q split, take
 // as long where the bus is full and longer elsewhere: four new tokens at 8000 keys
 // 15.2 us for 14.4, 64 dims at 64 by 8000 61 for 58.  Three workgroups a CU for 128
 // dims, 168 registers a lane: for four 42 spill.
