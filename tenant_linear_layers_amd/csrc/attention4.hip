@@ -9,7 +9,7 @@
 // over 16384 keys 266 us for 293, a prompt of 2048 85 for 89, mixed calls 0 to 5%
 // less).  But they keep a product to about 17 bits below the largest of its group: with
 // one dim of q at 512 or 1024 against keys of 4 the output's error was 0.012 to 0.017
-// and 0.030 to 0.043, so 0.0018, the roundings' own.
+// and 0.030 to 0.043; it is 0.0018 with exact ones, the roundings' own.
 //
 // Values.  The product with V runs over the keys, whose scales differ, so V is
 // converted everywhere.  A lane converts up to 16 bytes of a group by the
@@ -20,7 +20,6 @@
 #include "attention_plan.h"
 #include "common.h"
 #include "e2m1.h"
-#include "e4m3.h"
 #include "layer.h"
 
 namespace bd {
@@ -80,10 +79,8 @@ __device__ __forceinline__ void read_tr16_4(uint32_t at, u32x4 (&v)[4]) {
 //
 // Bound by HBM: 32 sequences of 8000 keys (279 MB) 57 us with their join, 4.9 TB/s
 // (a copy reaches 5.2), 64 of 1000 to 16000 (364 to 395 MB as they are drawn) 82 to
-// 91 by card.  A single token at 4097 keys, 8.3 us, is a chain of latencies.  Scaled products, with q split, take
-// as long where the bus is full and longer elsewhere: four new tokens at 8000 keys
-// 15.2 us for 14.4, 64 dims at 64 by 8000 61 for 58.  Three workgroups a CU for 128
-// dims, 168 registers a lane: for four 42 spill.
+// 91 by card.  A single token at 4097 keys, 8.3 us, is a chain of latencies.  Three
+// workgroups a CU for 128 dims, 168 registers a lane: for four 42 spill.
 template <int D, int NW>
 struct Few4 {
   // V in LDS: rows 32 bytes apart in the banks, so that the eight rows of a
